@@ -426,13 +426,13 @@ def _evict(st):
     mass[tp, h, to] = mass[fp, h, fo]
     pos[tp, h, to] = pos[fp, h, fo]
     st["length"].copy_(count)
-    # the sums of the pages that changed, and of the page the budget ends in
+    # the sums of the pages that changed, and of the last page where it is not full
     np_ = -(-n // page)
     pad = np_ * page - n
     row = torch.arange(np_ * page, device="cuda").view(1, 1, np_, page)
     changed = torch.nn.functional.pad((src != slot[..., :n]) & (src >= 0), (0, pad)).view(B, Hk, np_, page).any(-1)
     last = (row[..., 0] <= (count.view(B, 1, 1) - 1)) & (row[..., -1] >= count.view(B, 1, 1))
-    changed |= last & (len0 > n)
+    changed |= last
     pg = table[:, :np_]
     kp = k[pg].transpose(1, 2).float()  # [B, Hk, np_, page, d]
     total = torch.where((row < count.view(B, 1, 1, 1)).unsqueeze(-1), kp, 0.0).sum(dim=3)
@@ -606,7 +606,7 @@ def exact(case, seed):
             for name in ("k", "v", "mass", "pos"):
                 st[name][a] = st[name][z]
             dirty = to // page
-            if L[b] > m and m % page:
+            if m % page:
                 dirty = torch.cat([dirty, dirty.new_tensor([m // page])])
             dirty = torch.unique(dirty)
             ksum[table[b, dirty], h] = summed(b, h, dirty, m)
