@@ -10,6 +10,7 @@ Steps (AB-Attention news page, section «Три приёма AB-Attention»):
   select()         SIP sampling with inclusion-probability weights, or top-k
   attn_fwd()       block-sparse attention with Horvitz-Thompson weights (logit shift)
   attn_topk_fwd()  the same with all weights 1 (top-k baseline)
+Generation token by token over a key/value cache: ``cache.py`` (KVCache, cache_attn, ...).
 """
 
 from __future__ import annotations
@@ -20,7 +21,11 @@ from typing import Optional
 
 import torch
 
+from . import cache as _cache
 from . import synth  # noqa: F401  (seeded input generators)
+from .cache import (  # noqa: F401  (generation over a key/value cache)
+    FLAG_CACHE_FULL, MAX_TREE, AB_F16, KVCache, cache_append, cache_attn, cache_attn_workspace_bytes,
+    cache_compact, cache_keep, cache_mass, cache_score, make_cache)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libab_attn.so")
@@ -104,6 +109,7 @@ def lib():
                      "ab_selftest_attn_wait_limit", "ab_attn_bwd_workspace_size", "ab_attn_bwd",
                      "ab_selftest_attn_bwd_wait_limit"):
             getattr(L, name).restype = ctypes.c_int
+        _cache.bind(L)
         _lib = L
     return _lib
 

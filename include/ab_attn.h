@@ -58,7 +58,7 @@ typedef enum {
     AB_ERR_WORKSPACE = 10   /* workspace NULL or smaller than ab_score_workspace_size */
 } ab_status;
 
-typedef enum { AB_F32 = 0, AB_BF16 = 1 } ab_dtype;
+typedef enum { AB_F32 = 0, AB_BF16 = 1, AB_F16 = 2 /* the cache calls only */ } ab_dtype;
 
 typedef enum {
     AB_MODE_SIP = 0, /* sampling with inclusion-probability weights */
@@ -80,6 +80,7 @@ typedef struct {
 #define AB_FLAG_SCHED_COLLISION 16u /* ab_attn_*: another attention call used the same
                                        claim slot while this one ran (see "Scheduling" at
                                        ab_attn_fwd); this call's output is unreliable */
+#define AB_FLAG_CACHE_FULL 32u /* ab_cache_append: tokens past the table's capacity */
 
 /* Limits: head dim d in {64, 128}; 1 <= n_kb <= 8192 (N_pad <= 1,048,576). */
 #define AB_BLOCK 128
@@ -411,6 +412,176 @@ ab_status ab_forward_host(const void *q_host, const void *k_host, const void *v_
                           int n_clusters, int iters, ab_mode mode, int budget, uint64_t seed,
                           void *o_host, ab_dtype out_dtype, int chunk_heads, void *workspace,
                           size_t workspace_bytes, int *dev_flag, void *stream);
+
+/* ---------------------------------------------------------------------------------------
+ * Key/value cache: generation token by token over keys and values kept from earlier steps.
+ * The method's pages describe whole-sequence attention and mention an autoregressive
+ * relative that scores mean-pooled key blocks; the calls below carry both ideas over to a
+ * cache. A step of a serving program is
+ *   ab_cache_score -> ab_select -> ab_cache_attn (with the plan; without one it reads the
+ *   whole cache) -> ab_cache_append, and with a bounded cache ab_cache_mass after every
+ *   append and ab_cache_keep + ab_cache_compact when the cache is over its budget.
+ * They are forward-only: a gradient through whole sequences is ab_attn_bwd's.
+ *
+ * The cache of B sequences is a pool of n_pages pages of `page` tokens for Hk key heads,
+ * shared through a table: logical page i of sequence b is pool page table[b][i], slot s of
+ * the sequence is row s % page of logical page s / page, and slots 0 .. length[b] - 1 hold
+ * tokens. Hq = G * Hk query heads share the key heads in groups of G (query head h reads
+ * key head h / G). Query, key and value tensors of new tokens are [B, H, T, d] through
+ * strides (ab_tokens), so [B, T, H, d] storage is read as it is. Strides are in elements
+ * and multiples of 8; rows are contiguous. Addresses are computed in 64 bits.
+ * Per page and key head, ksum is the sum of the page's valid keys in a fixed order of
+ * additions (it depends on the page's keys alone, not on how they were appended); per slot
+ * and key head, mass is the attention weight received so far and pos the token's position.
+ * The calls raise AB_FLAG_BAD_INDEX for a length outside 0 .. max_pages * page (clamped),
+ * a token count outside 0 .. T (clamped) and a table entry outside 0 .. n_pages - 1 in a
+ * place that has to be read or written (the page is skipped).
+ * ------------------------------------------------------------------------------------- */
+#define AB_MAX_TREE 128 /* new tokens per sequence of ab_cache_attn / _score / _mass */
+
+typedef struct {
+    void *k, *v;          /* [n_pages, Hk, page, d] through the strides below */
+    float *ksum;          /* [n_pages, Hk, d] contiguous, or NULL */
+    float *mass;          /* [n_pages, Hk, page] contiguous, or NULL */
+    int32_t *pos;         /* [n_pages, Hk, page] contiguous, or NULL */
+    const int32_t *table; /* [B, max_pages] contiguous; entries behind a sequence's pages
+                             are not read */
+    int32_t *length;      /* [B] */
+    int64_t k_page, k_head, k_row, v_page, v_head, v_row; /* strides in elements */
+    int32_t B, Hk, d, page, n_pages, max_pages;           /* d 64 / 128; page 16, 32, 64, 128 */
+    int32_t dtype;                                        /* AB_BF16 or AB_F16 */
+} ab_cache;
+
+typedef struct {
+    const void *p;                         /* row (b, h, t) starts at b*sb + h*sh + t*st */
+    int64_t sb, sh, st;                    /* strides in elements */
+} ab_tokens;
+
+/*
+ * ab_cache_append -- write the keys and values of new tokens into the cache. Token i of
+ * sequence b (i < n_new[b]) comes from row sel[b][i] of k, v and goes to slot start[b] + i,
+ * with mass 0 and position pos0[b] + i; the ksum of every page that received a token is
+ * recomputed; length[b] = start[b] + n_new[b].
+ * k, v   : [B, Hk, T, d] of the cache's type. T: 1 .. 2^20.
+ * n_new  : int32 [B], or NULL for T each.
+ * sel    : int32 [B, T], or NULL for rows 0, 1, 2, ...: the accepted tokens of a drafted
+ *          tree, for instance. A row outside 0 .. T - 1 raises AB_FLAG_BAD_INDEX and is
+ *          written as zeros.
+ * start  : int32 [B] (not the cache's length array), or NULL to append at length. With it
+ *          the sequence is cut or kept at start[b] first: slots from start[b] + n_new[b]
+ *          on are no longer valid.
+ * pos0   : int32 [B], or NULL for start.
+ * Tokens that do not fit into max_pages * page slots are dropped (AB_FLAG_CACHE_FULL). A
+ * start outside 0 .. max_pages * page raises AB_FLAG_BAD_INDEX and leaves the sequence as
+ * it is. Different sequences must not share the pages that are written.
+ * Errors: AB_ERR_NULL, AB_ERR_SHAPE, AB_ERR_DTYPE, AB_ERR_UNSUPPORTED, AB_ERR_RANGE,
+ * AB_ERR_ALIGN, AB_ERR_CUDA (the same for the calls below).
+ */
+ab_status ab_cache_append(ab_cache c, ab_tokens k, ab_tokens v, int T, const int32_t *n_new,
+                          const int32_t *sel, const int32_t *start, const int32_t *pos0,
+                          int *dev_flag, void *stream);
+
+/*
+ * ab_cache_score -- a cheap score of every page for every query token: with
+ * x_{h,t,p} = q_{h,t} . ksum_p / (size_p sqrt(d)) (size_p valid tokens of page p),
+ *   scores[b][hk][t][p] = 1/G sum_{h in group hk} softmax_p(x_{h,t,.})  over the valid pages,
+ * so a row sums to 1, as ab_score's do, and goes to ab_select as it is (nkb = max_pages).
+ * The first `first` and last `recent` valid pages score 2, which SIP and top-k always keep
+ * while the budget is above their number. Pages behind the sequence score 0.
+ * q        : [B, Hq, T, d] of the cache's type. Hq: a multiple of Hk. T: 1 .. AB_MAX_TREE.
+ * n_tok    : int32 [B] valid tokens per sequence, or NULL for T; rows behind score 0.
+ * per_token: nonzero: one row per token, scores [B, Hk, T, max_pages]; zero: one row for all
+ *            tokens of a sequence, their mean, scores [B, Hk, 1, max_pages].
+ * scores   : out, fp32. max_pages <= AB_MAX_UNITS. Needs ksum.
+ */
+ab_status ab_cache_score(ab_cache c, ab_tokens q, int Hq, int T, const int32_t *n_tok,
+                         int per_token, int first, int recent, float *scores, int *dev_flag,
+                         void *stream);
+
+/*
+ * ab_cache_attn -- softmax attention of T new tokens per sequence over the cache and over
+ * each other. Token t of sequence b sees (i) the valid slots of every page, or of the pages
+ * of a plan, each with its logit shifted by ln w where the plan has weights, and (ii) new
+ * token j < n_tok[b] where tree[b][t][j] is set (without a tree: j <= t). A drafted tree
+ * sets tree[b][t][j] for t's ancestors j and t itself; one token is T = 1.
+ *   O_t = sum_s w_s e^{q_t.k_s/sqrt(d)} v_s / sum_s w_s e^{q_t.k_s/sqrt(d)}
+ * q         : [B, Hq, T, d]; k, v: [B, Hk, T, d] (k.p and v.p both NULL: no new tokens).
+ *             T: 1 .. AB_MAX_TREE.
+ * n_tok     : int32 [B], or NULL for T. tree: uint8 [B, T, T] (0 / 1), or NULL.
+ * idx, cnt, w : a plan as ab_select makes it from ab_cache_score's scores: idx int32
+ *             [B, Hk, Tp, max_pages] (distinct logical pages in the first cnt entries), cnt
+ *             int32 [B, Hk, Tp], w fp32 like idx or NULL for weights 1; Tp = T when
+ *             per_token is nonzero, else 1. idx NULL: every page. Kept pages behind the
+ *             sequence take no part; one outside 0 .. max_pages - 1 or a cnt outside
+ *             0 .. max_pages raises AB_FLAG_BAD_INDEX (skipped, clamped), a weight that is
+ *             not finite and positive AB_FLAG_BAD_WEIGHT (its page is skipped).
+ * out       : [B, Hq, T, d] contiguous, in the cache's type or AB_F32 (out_dtype); rows
+ *             t >= n_tok[b] and rows that see nothing are 0.
+ * lse       : optional fp32 [B, Hq, T]: ln of the denominator (0 for t >= n_tok[b], -inf
+ *             for a row that sees nothing).
+ * workspace : ab_cache_attn_workspace_size() bytes, contents need not be initialised. Calls
+ *             that may run at the same time need one each.
+ * The new tokens' own keys and values are read from k, v, not from the cache: append the
+ * accepted ones afterwards. Values in slots and rows that a sequence cannot see are never
+ * read; a value that some row of a (sequence, key head) sees takes part in that sequence's
+ * products, so a NaN or an infinity in a drafted token's value reaches its siblings.
+ * Every sum runs in an order that the lengths and counts fix: equal calls give equal bits.
+ */
+ab_status ab_cache_attn_workspace_size(ab_cache c, int Hq, int T, int per_token, size_t *bytes);
+ab_status ab_cache_attn(ab_cache c, ab_tokens q, ab_tokens k, ab_tokens v, int Hq, int T,
+                        const int32_t *n_tok, const uint8_t *tree, const int32_t *idx,
+                        const int32_t *cnt, const float *w, int per_token, void *out,
+                        ab_dtype out_dtype, float *lse, void *workspace, size_t workspace_bytes,
+                        int *dev_flag, void *stream);
+
+/*
+ * ab_cache_mass -- add the attention weight that every slot received from a sequence's
+ * newest tokens, after those were appended. With n = n_tok[b] of them, the i-th (row
+ * sel[b][i] of q and lse, or row i) sees slots s < length[b] - n + i + 1:
+ *   mass_out[s] = mass[s] + sum_{h in group, i} w e^{q_{h,i}.k_s/sqrt(d) - lse_{h,i}}.
+ * q, lse   : what ab_cache_attn was given and returned ([B, Hq, T, d], fp32 [B, Hq, T]
+ *            contiguous). sel: int32 [B, T] or NULL; a row outside 0 .. T - 1 raises
+ *            AB_FLAG_BAD_INDEX and adds nothing.
+ * idx, cnt, w, per_token : the plan of that call, or NULL; slots below length[b] - n outside
+ *            the row's pages get nothing from it. Plan rows are indexed as q's rows are.
+ * mass_out : NULL for the cache's mass (in place), or [n_pages, Hk, page]; slots behind a
+ *            sequence are not written. Needs mass.
+ */
+ab_status ab_cache_mass(ab_cache c, ab_tokens q, int Hq, int T, const int32_t *n_tok,
+                        const int32_t *sel, const float *lse, const int32_t *idx,
+                        const int32_t *cnt, const float *w, int per_token, float *mass_out,
+                        int *dev_flag, void *stream);
+
+/*
+ * ab_cache_keep -- which slots a cache bounded to `budget` slots per sequence keeps. Per
+ * (b, key head): the slots whose position is at least next_pos[b] - recent count as +inf;
+ * the m = min(length[b], budget) slots of the largest score stay, ties to the lower slot.
+ *   src[j] = j for a slot j < m that stays; the k-th slot below m that does not takes the
+ *   k-th kept slot s >= m (ascending); -1 for j >= m.
+ * So at most as many slots move as are evicted; the order of the slots is not the tokens'
+ * order afterwards (attention does not depend on it, and pos keeps the positions).
+ * score    : fp32 [n_pages, Hk, page], NULL for the cache's mass; a negative value or NaN
+ *            raises AB_FLAG_BAD_SCORE and counts as 0.
+ * pos      : int32 [n_pages, Hk, page], NULL for the cache's; not read when recent is 0.
+ * length   : int32 [B], NULL for the cache's. next_pos: int32 [B] (required when recent > 0).
+ * src      : out, int32 [B, Hk, budget]. n_keep: out, int32 [B]: m.
+ * workspace: ab_cache_keep_workspace_size() bytes.
+ */
+ab_status ab_cache_keep_workspace_size(ab_cache c, int budget, size_t *bytes);
+ab_status ab_cache_keep(ab_cache c, int budget, int recent, const int32_t *next_pos,
+                        const float *score, const int32_t *pos, const int32_t *length,
+                        int32_t *src, int32_t *n_keep, void *workspace, size_t workspace_bytes,
+                        int *dev_flag, void *stream);
+
+/*
+ * ab_cache_compact -- carry out ab_cache_keep's moves: the key, value, mass and pos of slot
+ * src[b][hk][j] go to slot j < n_keep[b]; the ksum of pages that changed, and of the last
+ * page where it is not full, is recomputed; length[b] = n_keep[b]. An entry below n_keep[b]
+ * that is neither j nor a slot >= n_keep[b] inside the table raises AB_FLAG_BAD_INDEX and
+ * is not moved.
+ */
+ab_status ab_cache_compact(ab_cache c, int budget, const int32_t *src, const int32_t *n_keep,
+                           int *dev_flag, void *stream);
 
 /*
  * ab_check_flag -- synchronise `stream`, copy *dev_flag to *host_flag and map it to a
