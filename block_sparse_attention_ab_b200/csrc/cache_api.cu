@@ -19,7 +19,7 @@ bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 
 // row starts must be 16-byte aligned; strides are kept small enough that a product with an
 // index stays inside 64 bits
-bool stride_ok(int64_t s) { return s % 8 == 0 && s >= 0 && s < (1ll << 40); }
+bool stride_ok(int64_t s) { return s % 8 == 0 && s >= 0 && s < (1ll << 38); }
 
 ab_status check_cache(const ab_cache &c, bool pages = true)
 {

@@ -20,73 +20,22 @@
 
 #include "cache_common.cuh"
 #include "cache_kernels.h"
+#include "cache_sched.cuh"
 
 namespace ab {
 namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kUnit = 16 * kWarps;   // keys per unit
-constexpr int kStage = 128;          // page slots staged at a time
-constexpr float kLazy = 8.f;         // the running maximum may lag by 2^8
-constexpr float kLn2 = 0.69314718055994531f;
-
-struct Staged {
-    int page;     // pool page, -1: takes no part
-    int valid;    // its valid rows
-    float shift;  // log2 of its weight
-};
-
-// Units and multiplicity of group `gi`: a sequence (without a plan) or a (b, hk, plan row).
-struct Group {
-    int b, hk, tp;      // hk -1: all key heads
-    int n;              // new tokens
-    int ctx;            // virtual keys of the cache: slots, or plan entries times page
-    int ctx_units, units, mult;
-};
-
-__device__ __forceinline__ Group load_group(const CacheAttn &a, int gi, int *flag)
-{
-    Group g;
-    g.tp = 0;
-    g.hk = -1;
-    g.mult = a.c.Hk;
-    if (a.idx) {
-        g.tp = gi % a.Tp;
-        const int bh = gi / a.Tp;
-        g.hk = bh % a.c.Hk;
-        g.b = bh / a.c.Hk;
-        g.mult = 1;
-    } else {
-        g.b = gi;
-    }
-    g.n = tok_count(a.n_tok, g.b, a.T, flag);
-    g.units = 0;
-    g.ctx = 0;
-    g.ctx_units = 0;
-    if (g.n == 0 || (a.per_token && g.tp >= g.n)) return g;
-    if (a.idx)
-        g.ctx = clamp_flag(a.cnt[gi], 0, a.c.max_pages, flag) * a.c.page;
-    else
-        g.ctx = cache_len(a.c, a.c.length, g.b, flag);
-    g.ctx_units = (g.ctx + kUnit - 1) / kUnit;
-    g.units = g.ctx_units + (a.k.p ? (g.n + kUnit - 1) / kUnit : 0);
-    return g;
-}
-
-__device__ __forceinline__ int group_rows(const CacheAttn &a, const Group &g)
-{
-    return a.per_token ? a.G : g.n * a.G;
-}
+constexpr int kStage = 128;  // page slots staged at a time
+static_assert(kUnit == 16 * kWarps, "a warp takes 16 keys of a unit");
 
 template <typename E, int D, int NT>
 struct Smem {
     Staged stage[kStage];
     float m[kWarps][8 * NT], l[kWarps][8 * NT];
     float merge[2][8 * NT][D];
-    long long scan[kThreads];
-    int found_group;
-    long long found_left;
+    RunSmem run;
 };
 
 template <typename E, int D, int NT, int OCC>
@@ -99,78 +48,11 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_attn_kernel(const CacheAt
     const int cta = blockIdx.x, nct = gridDim.x, rt = blockIdx.y;
     const int page = a.c.page, page_shift = a.page_shift;
 
-    // ---- this CTA's run of units [lo, hi) of the total, found by a scan of the groups
-    int gi;
-    long long left, in_group;  // units still to do; units of the group already behind us
-    if (a.whole_groups) {
-        gi = cta;
-        in_group = 0;
-        left = 0;
-    } else {
-        const int per = (a.groups + kThreads - 1) / kThreads;
-        long long mine = 0;
-        for (int i = tid * per; i < min((tid + 1) * per, a.groups); ++i) {
-            const Group gr = load_group(a, i, rt == 0 ? a.flag : nullptr);
-            mine += (long long)gr.units * gr.mult;
-        }
-        long long incl = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const long long y = __shfl_up_sync(~0u, incl, o);
-            if (lane >= o) incl += y;
-        }
-        if (lane == 31) sm.scan[warp] = incl;
-        if (tid == 0) sm.found_group = a.groups;
-        __syncthreads();
-        long long total = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            if (w < warp) incl += sm.scan[w];
-            total += sm.scan[w];
-        }
-        // at least one unit for every CTA that takes part: a row's parts lie in CTAs without
-        // a gap between them
-        const long long parts = min((long long)nct, total);
-        if (cta >= parts) return;
-        const long long lo = total * cta / parts, hi = total * (cta + 1) / parts;
-        if (lo >= incl - mine && lo < incl) {
-            long long at = incl - mine;
-            for (int i = tid * per;; ++i) {
-                const Group gr = load_group(a, i, nullptr);
-                const long long u = (long long)gr.units * gr.mult;
-                if (lo < at + u) {
-                    sm.found_group = i;
-                    sm.found_left = lo - at;
-                    break;
-                }
-                at += u;
-            }
-        }
-        __syncthreads();
-        gi = sm.found_group;
-        in_group = sm.found_left;
-        left = hi - lo;
-    }
-
-    for (; gi < a.groups;) {
-        const Group gr = load_group(a, gi, a.whole_groups && rt == 0 ? a.flag : nullptr);
-        const int rows = group_rows(a, gr);
-        int hk = gr.hk, u0 = 0, u1 = gr.units;
-        if (a.whole_groups) {
-            if (gr.units == 0) {
-                gi += nct;
-                continue;
-            }
-        } else {
-            if (in_group >= (long long)gr.units * gr.mult) {
-                in_group = 0;
-                ++gi;
-                continue;
-            }
-            if (hk < 0) hk = (int)(in_group / gr.units);
-            u0 = (int)(in_group % gr.units);
-            u1 = (int)min((long long)gr.units, u0 + left);
-        }
+    Run run = find_run<kThreads>(a, sm.run, cta, nct, rt == 0 ? a.flag : nullptr);
+    Piece pc;
+    while (next_piece(a, run, nct, pc, rt == 0 ? a.flag : nullptr)) {
+        const Group &gr = pc.g;
+        const int rows = group_rows(a, gr), hk = pc.hk, u0 = pc.u0, u1 = pc.u1;
         const int row0 = rt * 8 * NT;
         if (row0 < rows) {
             // ---- query fragments: row n = g of each tile of 8 (head fastest, then token)
@@ -250,30 +132,7 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_attn_kernel(const CacheAt
                 __syncthreads();
                 staged0 = (u * kUnit) >> page_shift;
                 for (int i = tid; i < kStage && staged0 + i < slots; i += kThreads) {
-                    Staged s = {-1, 0, 0.f};
-                    int lp = staged0 + i;
-                    bool use = true;
-                    if (a.idx) {
-                        const size_t at = (size_t)gi * a.c.max_pages + lp;
-                        lp = a.idx[at];
-                        if ((unsigned)lp >= (unsigned)a.c.max_pages) {
-                            raise_flag(a.flag, AB_FLAG_BAD_INDEX);
-                            use = false;
-                        }
-                        if (a.w) {
-                            const float w = a.w[at];
-                            if (!(w > 0.f && w < INFINITY)) {
-                                raise_flag(a.flag, AB_FLAG_BAD_WEIGHT);
-                                use = false;
-                            }
-                            s.shift = log2f(w);
-                        }
-                    }
-                    if (use && lp * page < cap) {
-                        s.page = cache_page(a.c, gr.b, lp, a.flag);
-                        s.valid = min(page, cap - lp * page);
-                    }
-                    sm.stage[i] = s;
+                    sm.stage[i] = stage_entry(a, pc, staged0 + i, cap);
                 }
                 __syncthreads();
             };
@@ -506,13 +365,6 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_attn_kernel(const CacheAt
             }
             __syncthreads();  // the merge buffers and the staged pages are free again
         }
-        if (a.whole_groups) {
-            gi += nct;
-        } else {
-            left -= u1 - u0;
-            in_group += u1 - u0;
-            if (left == 0) break;
-        }
     }
 }
 
@@ -595,14 +447,24 @@ template <typename E, int D, int NT, int OCC>
 cudaError_t launch_rows(const CacheAttn &a, int nct, cudaStream_t st)
 {
     auto kern = cache_attn_kernel<E, D, NT, OCC>;
-    const int smem = (int)sizeof(Smem<E, D, NT>);
-    if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-    }
-    kern<<<dim3(nct, a.row_tiles), kThreads, smem, st>>>(a);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
+    kern<<<dim3(nct, a.row_tiles), kThreads, sizeof(Smem<E, D, NT>), st>>>(a);
+    return cudaGetLastError();
+}
+
+template <typename E>
+cudaError_t launch_few(const CacheAttn &a, const CacheAttnPlan &p, cudaStream_t st)
+{
+    static_assert(sizeof(Smem<E, 128, 2>) <= 48 * 1024, "static limit");
+    if (a.c.d == 64)
+        return p.tile_rows == 8 ? launch_rows<E, 64, 1, 4>(a, p.ctas, st)
+                                : launch_rows<E, 64, 2, 3>(a, p.ctas, st);
+    return p.tile_rows == 8 ? launch_rows<E, 128, 1, 3>(a, p.ctas, st)
+                            : launch_rows<E, 128, 2, 2>(a, p.ctas, st);
+}
+
+template <typename E, int D>
+cudaError_t launch_join(const CacheAttn &a, const CacheAttnPlan &p, cudaStream_t st)
+{
     // programmatic launch: the join's CTAs start while the last units end and wait there
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(a.c.B * a.c.Hk * a.G * a.T);
@@ -613,17 +475,15 @@ cudaError_t launch_rows(const CacheAttn &a, int nct, cudaStream_t st)
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cache_join_kernel<E, D>, a, 8 * NT, nct);
+    return cudaLaunchKernelEx(&cfg, cache_join_kernel<E, D>, a, p.tile_rows, p.ctas);
 }
 
-template <typename E>
-cudaError_t launch_d(const CacheAttn &a, const CacheAttnPlan &p, cudaStream_t st)
+// A stride of 0 over more than one element (an expanded tensor) has no tensor map.
+bool strides_map(const ab_cache &c)
 {
-    if (a.c.d == 64)
-        return p.tile_rows == 8 ? launch_rows<E, 64, 1, 6>(a, p.ctas, st)
-                                : launch_rows<E, 64, 2, 4>(a, p.ctas, st);
-    return p.tile_rows == 8 ? launch_rows<E, 128, 1, 3>(a, p.ctas, st)
-                            : launch_rows<E, 128, 2, 2>(a, p.ctas, st);
+    auto ok = [](int64_t s, int n) { return s != 0 || n == 1; };
+    return ok(c.k_row, c.page) && ok(c.k_head, c.Hk) && ok(c.k_page, c.n_pages) && ok(c.v_row, c.page) &&
+           ok(c.v_head, c.Hk) && ok(c.v_page, c.n_pages);
 }
 
 }  // namespace
@@ -632,9 +492,17 @@ CacheAttnPlan cache_attn_plan(const ab_cache &c, int G, int T, bool per_token)
 {
     CacheAttnPlan p;
     const int rows = per_token ? G : G * T;
-    p.tile_rows = rows <= 8 ? 8 : 16;
+    int occ = 2;
+    if (rows > 16 && strides_map(c)) {
+        p.tile_rows = 128;
+    } else if (rows <= 8) {
+        p.tile_rows = 8;
+        occ = c.d == 64 ? 4 : 3;
+    } else {
+        p.tile_rows = 16;
+        occ = c.d == 64 ? 3 : 2;
+    }
     p.row_tiles = (rows + p.tile_rows - 1) / p.tile_rows;
-    const int occ = c.d == 64 ? (p.tile_rows == 8 ? 6 : 4) : (p.tile_rows == 8 ? 3 : 2);
     p.ctas = kCacheSms * occ / p.row_tiles;
     if (p.ctas < 1) p.ctas = 1;
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -656,7 +524,13 @@ cudaError_t launch_cache_attn(CacheAttn a, const CacheAttnPlan &p, void *workspa
     // Every CTA scans the groups to find its run of units. With very many of them the scan
     // would cost more than it evens out: then the CTAs take whole groups in turn.
     a.whole_groups = a.idx && a.groups > 8192;
-    return a.c.dtype == AB_F16 ? launch_d<Fp16>(a, p, st) : launch_d<Bf16>(a, p, st);
+    const bool h = a.c.dtype == AB_F16;
+    cudaError_t e = p.tile_rows == 128 ? launch_cache_tiles(a, p.ctas, st)
+                    : h                ? launch_few<Fp16>(a, p, st)
+                                       : launch_few<Bf16>(a, p, st);
+    if (e != cudaSuccess) return e;
+    if (a.c.d == 64) return h ? launch_join<Fp16, 64>(a, p, st) : launch_join<Bf16, 64>(a, p, st);
+    return h ? launch_join<Fp16, 128>(a, p, st) : launch_join<Bf16, 128>(a, p, st);
 }
 
 }  // namespace ab
