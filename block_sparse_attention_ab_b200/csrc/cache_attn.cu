@@ -494,7 +494,10 @@ CacheAttnPlan cache_attn_plan(const ab_cache &c, int G, int T, bool per_token)
     const int rows = per_token ? G : G * T;
     int occ = 2;
     if (rows > 16 && strides_map(c)) {
-        p.tile_rows = 128;
+        // up to three halves of 128 rows in one CTA (one CTA per SM), as evenly as they come
+        const int halves = (rows + 127) / 128, tiles = (halves + 2) / 3;
+        p.tile_rows = 128 * ((halves + tiles - 1) / tiles);
+        if (p.tile_rows > 128) occ = 1;
     } else if (rows <= 8) {
         p.tile_rows = 8;
         occ = c.d == 64 ? 4 : 3;
@@ -525,7 +528,7 @@ cudaError_t launch_cache_attn(CacheAttn a, const CacheAttnPlan &p, void *workspa
     // would cost more than it evens out: then the CTAs take whole groups in turn.
     a.whole_groups = a.idx && a.groups > 8192;
     const bool h = a.c.dtype == AB_F16;
-    cudaError_t e = p.tile_rows == 128 ? launch_cache_tiles(a, p.ctas, st)
+    cudaError_t e = p.tile_rows >= 128 ? launch_cache_tiles(a, p, st)
                     : h                ? launch_few<Fp16>(a, p, st)
                                        : launch_few<Bf16>(a, p, st);
     if (e != cudaSuccess) return e;

@@ -42,7 +42,7 @@ CacheAttnPlan cache_attn_plan(const ab_cache &c, int G, int T, bool per_token);
 cudaError_t launch_cache_attn(CacheAttn a, const CacheAttnPlan &p, void *workspace, cudaStream_t st);
 
 // many query rows per key head: the tile kernel (cache_tiles.cu), without the join
-cudaError_t launch_cache_tiles(const CacheAttn &a, int ctas, cudaStream_t st);
+cudaError_t launch_cache_tiles(const CacheAttn &a, const CacheAttnPlan &p, cudaStream_t st);
 
 cudaError_t launch_cache_append(const ab_cache &c, const ab_tokens &k, const ab_tokens &v, int T,
                                 const int32_t *n_new, const int32_t *sel, const int32_t *start,

@@ -65,8 +65,8 @@ struct Run {
     long long in_group, left;
 };
 
-struct RunSmem {
-    long long scan[8];
+struct RunSmem {  // up to 16 warps
+    long long scan[16];
     int group;
     long long in_group;
 };
@@ -76,6 +76,7 @@ struct RunSmem {
 template <int kThreads>
 __device__ __forceinline__ Run find_run(const CacheAttn &a, RunSmem &sm, int cta, int nct, int *flag)
 {
+    static_assert(kThreads / 32 <= 16, "RunSmem");
     Run run = {a.groups, 0, 0};
     if (a.whole_groups) {
         run.group = cta;

@@ -90,6 +90,12 @@ CASES = [
     ([2100, 4095, 1], 2, 2, 64, 16, 2, BF),
     ([90, 600], 1, 20, 128, 64, 9, FP),
     ([257], 1, 2, 128, 128, 100, BF),
+    # more than one half of 128 query rows, and rows in the last half for some sequences only
+    ([300, 900, 64], 1, 3, 128, 64, 86, FP),
+    ([1100, 33], 2, 5, 128, 32, 70, BF),
+    ([500], 1, 4, 64, 16, 127, BF),
+    ([1300, 2], 1, 12, 64, 128, 50, FP),
+    ([200], 1, 32, 128, 64, 12, BF),
 ]
 
 
