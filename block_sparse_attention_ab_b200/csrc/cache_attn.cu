@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_attn_kernel(const CacheAt
                 __syncthreads();
                 staged0 = (u * kUnit) >> page_shift;
                 for (int i = tid; i < kStage && staged0 + i < slots; i += kThreads) {
-                    sm.stage[i] = stage_entry(a, pc, staged0 + i, cap);
+                    sm.stage[i] = stage_entry(a, pc, staged0 + i, cap, a.flag);
                 }
                 __syncthreads();
             };
@@ -390,7 +390,10 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const CacheAttn a, int 
     if (!dead && !empty) {
         const int r = a.per_token ? h % a.G : t * a.G + h % a.G;
         const int rt = r / tile_rows, n = r % tile_rows;
-        const int2 who = a.info[((b * a.c.Hk + hk) * a.Tp + tp) * a.row_tiles + rt];
+        int2 who = a.info[((b * a.c.Hk + hk) * a.Tp + tp) * a.row_tiles + rt];
+        // inside the workspace even where a kernel gave up waiting before it wrote them
+        who.x = min(max(who.x, 0), nct - 1);
+        who.y = min(max(who.y, who.x), nct - 1);
         if (who.x == who.y) return;  // one CTA had it all and wrote it
         const int parts = who.y - who.x + 1;
         for (int p = warp; p < parts; p += 4) {
@@ -497,7 +500,7 @@ CacheAttnPlan cache_attn_plan(const ab_cache &c, int G, int T, bool per_token)
         // up to three halves of 128 rows in one CTA (one CTA per SM), as evenly as they come
         const int halves = (rows + 127) / 128, tiles = (halves + 2) / 3;
         p.tile_rows = 128 * ((halves + tiles - 1) / tiles);
-        if (p.tile_rows > 128) occ = 1;
+        occ = 1;
     } else if (rows <= 8) {
         p.tile_rows = 8;
         occ = c.d == 64 ? 4 : 3;

@@ -165,7 +165,7 @@ __device__ __forceinline__ bool next_piece(const CacheAttn &a, Run &run, int nct
 }
 
 // Page slot `slot` of the piece's context as the kernels use it. cap: the sequence's length.
-__device__ __forceinline__ Staged stage_entry(const CacheAttn &a, const Piece &p, int slot, int cap)
+__device__ __forceinline__ Staged stage_entry(const CacheAttn &a, const Piece &p, int slot, int cap, int *flag)
 {
     Staged s = {-1, 0, 0.f};
     int lp = slot;
@@ -173,20 +173,20 @@ __device__ __forceinline__ Staged stage_entry(const CacheAttn &a, const Piece &p
         const size_t at = (size_t)p.gi * a.c.max_pages + slot;
         lp = a.idx[at];
         if ((unsigned)lp >= (unsigned)a.c.max_pages) {
-            raise_flag(a.flag, AB_FLAG_BAD_INDEX);
+            raise_flag(flag, AB_FLAG_BAD_INDEX);
             return s;
         }
         if (a.w) {
             const float w = a.w[at];
             if (!(w > 0.f && w < INFINITY)) {
-                raise_flag(a.flag, AB_FLAG_BAD_WEIGHT);
+                raise_flag(flag, AB_FLAG_BAD_WEIGHT);
                 return s;
             }
             s.shift = log2f(w);
         }
     }
     if (lp * a.c.page < cap) {
-        s.page = cache_page(a.c, p.g.b, lp, a.flag);
+        s.page = cache_page(a.c, p.g.b, lp, flag);
         s.valid = min(a.c.page, cap - lp * a.c.page);
     }
     return s;

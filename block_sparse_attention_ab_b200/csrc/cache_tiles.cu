@@ -1,20 +1,20 @@
 // cache_tiles.cu -- ab_cache_attn for many query rows per key head (a tree of drafted tokens
 // times the heads that share a key head): the 5th-generation tensor core.
 //
-// One CTA holds one to three halves of 128 query rows and walks units of 64 keys
-// (cache_sched.cuh); for each half in turn
-//   S = Q K^T (128 x 64) -> softmax in registers, a thread per row, four warps per half ->
-//   P over S's own tensor memory -> O += P V (128 x d, fp32 in tensor memory).
-// S has several buffers, so the products of the next halves run while a half's threads work
-// on theirs. With one half two CTAs share an SM; with two or three, every tile of keys is
-// read once for all of them (320 rows: 3 halves fill tensor memory, 384 columns of O and two
-// S buffers, against three CTAs that read it three times). Units whose 64 keys all
-// exist come by TMA through a map over (d, row, head, page): the page's number is a coordinate,
-// so any strides and page sizes do, and pages of 16 and 32 tokens are 4 and 2 boxes of one
-// tile. The others (a sequence's last keys, the new tokens, a tile with an absent page) are
-// written by the softmax threads themselves, with zeros where no key is, in the same swizzle;
-// a run is walked from its end, so that this happens while the first copies are on their way.
-// CTAs of the row tiles of one key head take the same runs and share K and V in L2.
+// One CTA per SM holds one to three halves of 128 query rows and walks units of 64 keys
+// (cache_sched.cuh), so a key tile is read once for up to 384 rows. For each half in turn
+//   S = Q K^T (128 x 64, in one of a few tensor memory buffers) -> softmax in registers, four
+//   warps per half, a thread per row -> P (shared memory) -> O += P V (tensor memory, fp32).
+// S leaves its buffer as soon as a half's threads have loaded it, so two buffers serve three
+// halves (their accumulators fill the other 384 of 512 columns) and every half's threads find
+// their next S waiting. (P written over S instead, the buffer held until the second product:
+// 490 us against {TILE_US} us for a 64-token tree over 8 x 16001..32760 slots, 40 / 8 heads.)
+// Units whose 64 keys all exist come by TMA through a map over (d, row, head, page): the page's
+// number is a coordinate, so any strides and page sizes do, and pages of 16 and 32 tokens are 4
+// and 2 boxes of one tile. The others (a sequence's last keys, the new tokens, a tile with an
+// absent page) are written by the first half's threads themselves, with zeros where no key is,
+// in the same swizzle; a run is walked from its end, so that this happens while the first
+// copies are on their way.
 #include <cstdint>
 
 #include "cache_common.cuh"
@@ -30,36 +30,50 @@ constexpr int kEnt = 4;                    // page slots of a unit, at most (16-
 
 struct TileInfo {
     Staged ent[kEnt];
-    int manual;  // the softmax threads write this unit's tile
+    int manual;  // the first half's threads write this unit's tiles
 };
 
-// NH halves; tensor memory: kSBufs S buffers of 64 columns, then NH accumulators of D.
+// NH halves. Tensor memory: kSBufs S buffers of 64 columns, then NH accumulators of D.
+// Shared memory: Q and P of every half, a ring of K tiles and one of V tiles. Four warps
+// beside the softmax: one copies K, one V, one issues S = Q K^T, one O += P V. Each waits for
+// its own needs only, so neither a late copy nor a late P holds back anything else, and each
+// warp's loop is short enough to keep ahead of the tensor core (all four roles in one polling
+// warp: 510 us for the case above).
 template <int D, int NH>
 struct TileSmem {
-    static constexpr int kThreads = NH * 128 + 64;  // four softmax warps per half, TMA, MMA
-    static constexpr int kWarpTma = NH * 4, kWarpMma = NH * 4 + 1;
-    static constexpr int kSBufs = NH == 1 ? 2 : NH == 2 ? 4 : D == 128 ? 2 : 4;
+    static constexpr int kThreads = NH * 128 + 128;  // four softmax warps per half
+    static constexpr int kWarpK = NH * 4, kWarpV = kWarpK + 1, kWarpS = kWarpK + 2, kWarpO = kWarpK + 3;
+    static constexpr int kSBufs = NH == 3 && D == 128 ? 2 : 4;
     static constexpr int kColO = kSBufs * kUnit;
-    static constexpr int kTmemCols = NH == 1 ? 256 : 512;
+    static constexpr int kTmemCols = 512;
     static_assert(kColO + NH * D <= kTmemCols, "tensor memory");
-    static constexpr int kStages = (D == 128 ? (NH == 1 ? 2 : 7 - NH) : (NH == 1 ? 4 : 8));
     static constexpr int kBoxes = D / 64;
     static constexpr int kQHalf = kRows * D * 2;
-    static constexpr int kQBytes = NH * kQHalf;
+    static constexpr int kPHalf = kRows * kUnit * 2;
     static constexpr int kTile = kUnit * D * 2;  // one K or V tile
-    static constexpr int kKv = kQBytes;          // [stage][K, V]
-    static constexpr int kInfo = kKv + kStages * 2 * kTile;
-    static constexpr int kBars = (kInfo + kStages * (int)sizeof(TileInfo) + 7) / 8 * 8;
-    // info_full, kv_full, filled, kv_empty [stages], s_full [NH][2], p_full [kSBufs], q_full,
-    // pv_done [NH], drain. A parity wait is exact for a waiter that sees every phase: s_full
-    // belongs to a half (its even and odd units), p_full to the MMA warp, which waits for
-    // every job in turn.
-    static constexpr int kNumBars = 4 * kStages + 2 * NH + kSBufs + 2 * NH + 1;
-    static constexpr int kMisc = kBars + kNumBars * 8;  // tensor memory address, abort flag
+    static constexpr int kP = NH * kQHalf;
+    static constexpr int kKv = kP + NH * kPHalf;
+    static constexpr int kFit = (224 * 1024 - kKv) / kTile, kSlots = kFit > 10 ? 10 : kFit;
+    static constexpr int kK = kSlots / 2, kV = kSlots - kK;  // V is held longer
+    static constexpr int kVAt = kKv + kK * kTile;
+    // A unit's info is read until its second product is issued. K of unit i is loaded when S of
+    // unit i - kK is done; S runs at most 4 units (the S buffers) ahead of the loads from its
+    // buffers, and those 2 units ahead of the second products
+    static constexpr int kInfos = 16;
+    static_assert(kK >= 2 && kK + 4 + 2 <= kInfos, "ring");
+    static constexpr int kInfo = kKv + kSlots * kTile;
+    static constexpr int kBars = (kInfo + kInfos * (int)sizeof(TileInfo) + 7) / 8 * 8;
+    // filled [kInfos], kv_full, kv_empty [kSlots], s_free [kSBufs], s_full [NH][4], p_full,
+    // q_full, pv_done [NH], drain [2]. A parity wait is exact for a waiter that sees every phase:
+    // s_full (its units in turn) and pv_done belong to a half, the others to one of the
+    // four warps, which waits for every use in turn. Units published are counted instead: a
+    // half without rows in a piece does not follow it.
+    static constexpr int kNumBars = kInfos + 2 * kSlots + kSBufs + 7 * NH + 2;
+    static constexpr int kMisc = kBars + kNumBars * 8;  // tensor memory address, counts, abort flag
     static constexpr int kRun = kMisc + 16;
     static constexpr int kBytes = kRun + (int)sizeof(RunSmem);
     static constexpr int kAlloc = kBytes + 1024;
-    static_assert(kAlloc <= (NH == 1 ? 113 : 227) * 1024, "shared memory");
+    static_assert(kAlloc <= 227 * 1024, "shared memory");
 };
 
 __device__ __forceinline__ void tma_load_4d(void *smem_dst, const void *tmap, uint64_t *bar, int x,
@@ -72,6 +86,35 @@ __device__ __forceinline__ void tma_load_4d(void *smem_dst, const void *tmap, ui
         : "memory");
 }
 
+__device__ __forceinline__ void store_release(int *p, int v)
+{
+    asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
+}
+
+__device__ __forceinline__ int load_acquire(const int *p)
+{
+    int v;
+    asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(v) : "r"(smem_u32(p)) : "memory");
+    return v;
+}
+
+// Wait until *p is above n; gives up as mbar_wait does.
+__device__ __forceinline__ bool wait_count(int *p, int n, volatile int *abort, int *flag)
+{
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t spin = 0;; ++spin) {
+        if (load_acquire(p) > n) return true;
+        if ((spin & 63u) == 63u) {
+            if (*abort) return false;
+            if (global_timer_ns() - t0 > kWaitLimitNs) {
+                *abort = 1;
+                raise_flag(flag, AB_FLAG_TIMEOUT);
+                return false;
+            }
+        }
+    }
+}
+
 template <typename E>
 constexpr uint32_t idesc(int M, int N, int a_mn, int b_mn)
 {
@@ -79,47 +122,50 @@ constexpr uint32_t idesc(int M, int N, int a_mn, int b_mn)
 }
 
 template <typename E, int D, int NH>
-__global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, NH == 1 ? 2 : 1)
+__global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
     cache_tile_kernel(const CacheAttn a, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV)
 {
     using L = TileSmem<D, NH>;
-    constexpr int NS = L::kStages, SB = L::kSBufs, kColO = L::kColO;
+    constexpr int NK = L::kK, NV = L::kV, NI = L::kInfos, SB = L::kSBufs;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t *smem = align_smem_1024(smem_raw);
     TileInfo *info = reinterpret_cast<TileInfo *>(smem + L::kInfo);
-    uint64_t *info_full = reinterpret_cast<uint64_t *>(smem + L::kBars);
-    uint64_t *kv_full = info_full + NS;  // by TMA
-    uint64_t *filled = kv_full + NS;     // by the softmax threads
-    uint64_t *kv_empty = filled + NS;
-    uint64_t *s_full = kv_empty + NS, *p_full = s_full + 2 * NH;
-    uint64_t *q_full = p_full + SB, *pv_done = q_full + NH, *drain = pv_done + NH;
+    uint64_t *filled = reinterpret_cast<uint64_t *>(smem + L::kBars);  // tiles by the softmax threads
+    uint64_t *k_full = filled + NI, *v_full = k_full + NK;  // a tile copied by TMA
+    uint64_t *k_empty = v_full + NV, *v_empty = k_empty + NK, *s_free = v_empty + NV, *s_full = s_free + SB;
+    uint64_t *p_full = s_full + 4 * NH, *q_full = p_full + NH, *pv_done = q_full + NH;
+    uint64_t *drain = pv_done + NH;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMisc);
-    volatile int *abort = reinterpret_cast<volatile int *>(smem + L::kMisc + 8);
+    int *published = reinterpret_cast<int *>(smem + L::kMisc + 4);  // units whose info and K slot are there
+    int *v_slots = reinterpret_cast<int *>(smem + L::kMisc + 8);    // units whose V slot is free
+    volatile int *abort = reinterpret_cast<volatile int *>(smem + L::kMisc + 12);
     RunSmem &run_sm = *reinterpret_cast<RunSmem *>(smem + L::kRun);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = blockIdx.x, nct = gridDim.x, rt = blockIdx.y, row0 = rt * NH * kRows;
     const int page = a.c.page, shift = a.page_shift;
 
     if (tid == 0) {
-        for (int s = 0; s < NS; ++s) {
-            mbar_init(&info_full[s], 1);
-            mbar_init(&kv_full[s], 1);
-            mbar_init(&filled[s], 128);
-            mbar_init(&kv_empty[s], 1);
+        for (int i = 0; i < NI; ++i) mbar_init(&filled[i], 128);
+        for (int s = 0; s < L::kSlots; ++s) {
+            mbar_init(&k_full[s], 1);   // and v_full behind it
+            mbar_init(&k_empty[s], 1);  // and v_empty
         }
-        for (int s = 0; s < SB; ++s) mbar_init(&p_full[s], 128);
+        for (int s = 0; s < SB; ++s) mbar_init(&s_free[s], 4);
         for (int h = 0; h < NH; ++h) {
-            mbar_init(&s_full[2 * h], 1);
-            mbar_init(&s_full[2 * h + 1], 1);
+            for (int i = 0; i < 4; ++i) mbar_init(&s_full[4 * h + i], 1);
+            mbar_init(&p_full[h], 4);
             mbar_init(&q_full[h], 128);
             mbar_init(&pv_done[h], 1);
         }
-        mbar_init(drain, 1);
+        mbar_init(&drain[0], 1);
+        mbar_init(&drain[1], 1);
         *abort = 0;
+        *published = 0;
+        *v_slots = 0;
         fence_barrier_init();
     }
-    if (warp == L::kWarpMma) {
+    if (warp == L::kWarpS) {
         tmem_alloc(tmem_slot, L::kTmemCols);
         tmem_relinquish();
     }
@@ -131,136 +177,189 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, NH == 1 ? 2 : 1)
     const uint32_t tmem = *tmem_slot;
     Piece pc;
 
-    auto wait = [&](uint64_t *bar, int n) -> bool {  // phase n of bar
-        return __all_sync(~0u, mbar_wait(bar, n & 1, abort, a.flag));
+    auto wait = [&](uint64_t *bar, uint32_t phase) -> bool {
+        return __all_sync(~0u, mbar_wait(bar, phase & 1, abort, a.flag));
+    };
+    auto wait_for = [&](int *count, int unit) -> bool {
+        return __all_sync(~0u, wait_count(count, unit, abort, a.flag));
     };
 
-    if (warp == L::kWarpTma) {
-        if (elect_one()) {
-            prefetch_tmap(&tmK);
-            prefetch_tmap(&tmV);
-        }
+    if (warp == L::kWarpK || warp == L::kWarpV) {
+        const bool is_k = warp == L::kWarpK;
+        const CUtensorMap *tm = is_k ? &tmK : &tmV;
+        uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
+        uint8_t *ring = smem + (is_k ? L::kKv : L::kVAt);
+        const int ns = is_k ? NK : NV;
+        if (elect_one()) prefetch_tmap(tm);
         __syncwarp();
         const int nent = max(1, kUnit >> shift), box_rows = min(page, kUnit);
-        int it = 0;
-        uint32_t phase = 0, loaded = 0;  // bit s: parity of stage s's next copy; its last unit came by TMA
+        // the lanes look up 32 / nent units together, so that a table (and a plan) is waited
+        // for once in so many units
+        const int batch = 32 / nent;
+        int it = 0, s = 0;                  // units so far, their ring slot
+        uint32_t par_e = 1;                 // parity of the slots' last release
+        uint32_t phase = 0, loaded = 0;     // bit s: parity of slot s's next copy; its last use was a copy
         bool ok = true;
         while (ok && next_piece(a, run, nct, pc, nullptr)) {
             if (row0 >= group_rows(a, pc.g)) continue;
-            const int cap = cache_len(a.c, a.c.length, pc.g.b, flag0);
+            const int cap = cache_len(a.c, a.c.length, pc.g.b, is_k ? flag0 : nullptr);
             const int slots = (pc.g.ctx + page - 1) >> shift;
-            for (int u = pc.u1 - 1; ok && u >= pc.u0; --u, ++it) {
-                const int s = it % NS;
-                Staged e = {-1, 0, 0.f};
-                const int slot = ((u * kUnit) >> shift) + lane;
-                const bool ctx = u < pc.g.ctx_units;
-                if (ctx && lane < nent && slot < slots) e = stage_entry(a, pc, slot, cap);
+            Staged eb = {-1, 0, 0.f};
+            int behind = batch;  // units of the batch that are done
+            for (int u = pc.u1 - 1; ok && u >= pc.u0; --u, ++it, ++behind) {
+                if (behind == batch) {
+                    behind = 0;
+                    eb = {-1, 0, 0.f};
+                    const int uu = u - lane / nent, slot = ((uu * kUnit) >> shift) + lane % nent;
+                    if (uu >= pc.u0 && uu < pc.g.ctx_units && slot < slots)
+                        eb = stage_entry(a, pc, slot, cap, is_k ? a.flag : nullptr);
+                }
+                const int from = (behind * nent + lane) & 31;
+                Staged e;
+                e.page = __shfl_sync(~0u, eb.page, from);
+                e.valid = __shfl_sync(~0u, eb.valid, from);
+                e.shift = __shfl_sync(~0u, eb.shift, from);
                 const int r0 = page > kUnit ? (u * kUnit) & (page - 1) : 0;
                 const bool clean = lane >= nent || (e.page >= 0 && e.valid >= r0 + box_rows);
                 const bool manual = !__all_sync(~0u, clean);
-                if (it >= NS) ok = wait(&kv_empty[s], it / NS - 1);
+                if (it >= ns) ok = wait(&empty[s], par_e);
                 if (!ok) break;
-                if (lane < nent) info[s].ent[lane] = e;
-                if (lane == 0) info[s].manual = manual;
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&info_full[s]);
-                    if (!manual) mbar_arrive_expect_tx(&kv_full[s], 2 * L::kTile);
+                if (is_k) {
+                    TileInfo &ti = info[it % NI];
+                    if (lane < nent) ti.ent[lane] = e;
+                    if (lane == 0) ti.manual = manual;
+                    __syncwarp();
                 }
-                __syncwarp();
-                loaded = manual ? loaded & ~(1u << s) : loaded | 1u << s;
-                if (!manual) phase ^= 1u << s;
-                if (!manual && lane < nent) {
-                    uint8_t *k = smem + L::kKv + s * 2 * L::kTile + lane * box_rows * 128;
+                if (lane == 0) store_release(is_k ? published : v_slots, it + 1);
+                if (manual) {
+                    loaded &= ~(1u << s);
+                } else {
+                    if (lane == 0) mbar_arrive_expect_tx(&full[s], L::kTile);
+                    __syncwarp();
+                    loaded |= 1u << s;
+                    phase ^= 1u << s;
+                    if (lane < nent) {
+                        uint8_t *d = ring + s * L::kTile + lane * box_rows * 128;
 #pragma unroll
-                    for (int x = 0; x < L::kBoxes; ++x)
-                        tma_load_4d(k + x * (kUnit * 128), &tmK, &kv_full[s], x * 64, r0, pc.hk, e.page);
-#pragma unroll
-                    for (int x = 0; x < L::kBoxes; ++x)
-                        tma_load_4d(k + L::kTile + x * (kUnit * 128), &tmV, &kv_full[s], x * 64, r0, pc.hk,
-                                    e.page);
+                        for (int y = 0; y < L::kBoxes; ++y)
+                            tma_load_4d(d + y * (kUnit * 128), tm, &full[s], y * 64, r0, pc.hk, e.page);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
+                if (++s == ns) {
+                    s = 0;
+                    par_e ^= 1;
+                }
             }
         }
         if (!ok) {  // copies that may still be in flight land before the CTA ends
-            for (int s = 0; s < NS; ++s)
-                if (loaded >> s & 1) drain_wait(&kv_full[s], (phase >> s & 1) ^ 1);
+            for (int x = 0; x < ns; ++x)
+                if (loaded >> x & 1) drain_wait(&full[x], (phase >> x & 1) ^ 1);
         }
-    } else if (warp == L::kWarpMma) {
-        constexpr uint32_t idesc_s = idesc<E>(kRows, kUnit, 0, 0), idesc_o = idesc<E>(kRows, D, 0, 1);
+    } else if (warp == L::kWarpS) {
+        constexpr uint32_t idesc_s = idesc<E>(kRows, kUnit, 0, 0);
         const uint64_t qd = smem_desc_sw128(smem_u32(smem), 16, 1024);
         const uint64_t kd0 = smem_desc_sw128(smem_u32(smem + L::kKv), 16, 1024);
-        const uint64_t vd0 = smem_desc_sw128(smem_u32(smem + L::kKv + L::kTile), kUnit * 128, 1024);
-        int it = 0, job = 0;  // units and (unit, half) jobs before this piece
-        uint32_t copied = 0, written = 0;  // bit s: parity of stage s's next copy / next written tile
-        uint32_t qphase = 0;               // bit h: parity of half h's next Q
-        uint32_t odd = 0;                  // bit h: half h's next unit is an odd one of its own
-        bool ok = true;
-        int na = 1;  // halves with rows in this piece
-        // job j of the piece: unit j / na, half j % na
-        auto issue_s = [&](int j) {
-            const int i = it + j / na, h = j % na, s = i % NS, buf = (job + j) % SB;
-            if (h == 0) {
-                if (!wait(&info_full[s], i / NS)) return false;
-                const bool manual = info[s].manual;
-                if (!(manual ? wait(&filled[s], written >> s) : wait(&kv_full[s], copied >> s))) return false;
-                if (manual)
-                    written ^= 1u << s;
-                else
-                    copied ^= 1u << s;
-                tc_fence_after();
-            }
-            const uint64_t kd = kd0 + (uint64_t)s * (2 * L::kTile >> 4);
-            const uint64_t qh = qd + (uint64_t)h * (L::kQHalf >> 4);
-            if (elect_one()) {
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
-                    mma_ss(tmem + buf * kUnit, qh + ((kk >> 2) * (kRows * 128) + (kk & 3) * 32 >> 4),
-                           kd + ((kk >> 2) * (kUnit * 128) + (kk & 3) * 32 >> 4), idesc_s, kk > 0);
-                mma_commit(&s_full[2 * h + (odd >> h & 1)]);
-            }
-            odd ^= 1u << h;
-            __syncwarp();
-            return true;
-        };
+        int it = 0, s = 0;                // units so far, their ring slot
+        int buf = 0;                      // S buffer of the next job
+        uint32_t copied = 0;              // bit s: parity of slot s's next copy
+        uint32_t written = 0;             // bit i: parity of info slot i's next written unit
+        uint32_t turn = 0, phase_q = 0;   // two bits per half: its next S's barrier; bit h: its next Q
+        uint32_t par_b = 1;               // parity of the S buffers' last release
+        bool ok = true, used = false;     // used: every S buffer has had a job
         while (ok && next_piece(a, run, nct, pc, nullptr)) {
             const int rows = group_rows(a, pc.g) - row0;
             if (rows <= 0) continue;
-            na = min(NH, (rows + kRows - 1) / kRows);
-            const int n = (pc.u1 - pc.u0) * na;
+            const int na = min(NH, (rows + kRows - 1) / kRows);  // halves with rows in this piece
             for (int h = 0; ok && h < na; ++h) {
-                ok = wait(&q_full[h], qphase >> h);
-                qphase ^= 1u << h;
+                ok = wait(&q_full[h], phase_q >> h);
+                phase_q ^= 1u << h;
             }
-            tc_fence_after();
-            // S products ahead of the softmax: as many as there are buffers, two per half
-            const int ahead = min(SB, 2 * na);
-            for (int j = 0; ok && j < min(ahead, n); ++j) ok = issue_s(j);
-            for (int j = 0; ok && j < n; ++j) {
-                const int buf = (job + j) % SB, h = j % na, s = (it + j / na) % NS;
-                ok = wait(&p_full[buf], (job + j) / SB);
+            for (int n = pc.u1 - pc.u0; ok && n > 0; --n, ++it) {
+                const int ii = it % NI;
+                ok = wait_for(published, it);
                 if (!ok) break;
-                tc_fence_after();
-                const uint64_t vd = vd0 + (uint64_t)s * (2 * L::kTile >> 4);
-                if (elect_one()) {
-#pragma unroll
-                    for (int kk = 0; kk < kUnit / 16; ++kk)
-                        mma_ts(tmem + kColO + h * D, tmem + buf * kUnit + kk * 8, vd + (kk * 2048 >> 4), idesc_o,
-                               j >= na || kk > 0);
-                    mma_commit(&pv_done[h]);
-                    if (h == na - 1) mma_commit(&kv_empty[s]);
+                if (info[ii].manual) {
+                    ok = wait(&filled[ii], written >> ii);
+                    written ^= 1u << ii;
+                } else {
+                    ok = wait(&k_full[s], copied >> s);
+                    copied ^= 1u << s;
                 }
-                __syncwarp();
-                if (j + ahead < n) ok = issue_s(j + ahead);
+                const uint64_t kd = kd0 + (uint64_t)s * (L::kTile >> 4);
+                for (int h = 0; ok && h < na; ++h) {
+                    if (used) ok = wait(&s_free[buf], par_b);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t qh = qd + (uint64_t)h * (L::kQHalf >> 4);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk)
+                            mma_ss(tmem + buf * kUnit, qh + ((kk >> 2) * (kRows * 128) + (kk & 3) * 32 >> 4),
+                                   kd + ((kk >> 2) * (kUnit * 128) + (kk & 3) * 32 >> 4), idesc_s, kk > 0);
+                        mma_commit(&s_full[4 * h + (turn >> 2 * h & 3)]);
+                        if (h == na - 1) mma_commit(&k_empty[s]);
+                    }
+                    __syncwarp();
+                    turn = (turn & ~(3u << 2 * h)) | ((turn + (1u << 2 * h)) & (3u << 2 * h));
+                    if (++buf == SB) {
+                        buf = 0;
+                        used = true;
+                        par_b ^= 1;
+                    }
+                }
+                if (++s == NK) s = 0;
             }
-            it += pc.u1 - pc.u0;
-            job += n;
         }
         if (!ok) {
             if (elect_one()) {
-                mma_commit(drain);
-                drain_wait(drain, 0);
+                mma_commit(&drain[0]);
+                drain_wait(&drain[0], 0);
+            }
+            __syncwarp();
+        }
+    } else if (warp == L::kWarpO) {
+        constexpr uint32_t idesc_o = idesc<E>(kRows, D, 0, 1);
+        const uint64_t pd = smem_desc_sw128(smem_u32(smem + L::kP), 16, 1024);
+        const uint64_t vd0 = smem_desc_sw128(smem_u32(smem + L::kVAt), kUnit * 128, 1024);
+        int it = 0, s = 0;
+        uint32_t copied = 0, phase_p = 0;  // bit s: slot s's next copy; bit h: half h's next P
+        bool ok = true;
+        while (ok && next_piece(a, run, nct, pc, nullptr)) {
+            const int rows = group_rows(a, pc.g) - row0;
+            if (rows <= 0) continue;
+            const int na = min(NH, (rows + kRows - 1) / kRows);
+            for (int n = 0; ok && n < pc.u1 - pc.u0; ++n, ++it) {
+                // a unit that the threads wrote is there when its P is
+                ok = wait_for(published, it);
+                if (ok && !info[it % NI].manual) {
+                    ok = wait(&v_full[s], copied >> s);
+                    copied ^= 1u << s;
+                }
+                const uint64_t vd = vd0 + (uint64_t)s * (L::kTile >> 4);
+                for (int h = 0; ok && h < na; ++h) {
+                    ok = wait(&p_full[h], phase_p >> h);
+                    if (!ok) break;
+                    phase_p ^= 1u << h;
+                    tc_fence_after();
+                    const uint64_t ph = pd + (uint64_t)h * (L::kPHalf >> 4);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kk = 0; kk < kUnit / 16; ++kk)
+                            mma_ss(tmem + L::kColO + h * D, ph + (kk * 32 >> 4), vd + (kk * 2048 >> 4), idesc_o,
+                                   n > 0 || kk > 0);
+                        mma_commit(&pv_done[h]);
+                        if (h == na - 1) mma_commit(&v_empty[s]);
+                    }
+                    __syncwarp();
+                }
+                if (++s == NV) s = 0;
+            }
+        }
+        if (!ok) {
+            if (elect_one()) {
+                mma_commit(&drain[1]);
+                drain_wait(&drain[1], 0);
             }
             __syncwarp();
         }
@@ -268,21 +367,23 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, NH == 1 ? 2 : 1)
         // ---- softmax: thread = query row. After a failed wait a warp runs out its loops
         // without waiting, and reads no page.
         bool ok = true;
-        auto wait_on = [&](uint64_t *bar, int n) {
-            if (ok) ok = wait(bar, n);
+        auto wait_on = [&](uint64_t *bar, uint32_t phase) {
+            if (ok) ok = wait(bar, phase);
         };
         const int half = warp >> 2, th = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t acc = tmem + lanes + kColO + half * D;
+        const uint32_t acc = tmem + lanes + L::kColO + half * D;
+        uint8_t *prow = smem + L::kP + half * L::kPHalf + th * 128;
+        const float inv_scale = 1.f / a.scale_log2;
         int it = 0, job = 0;  // units and jobs before this piece
-        int pv = 0;           // products of this half so far
+        int pv = 0;           // units of this half so far
         while (next_piece(a, run, nct, pc, half == 0 ? flag0 : nullptr)) {
             const int rows = group_rows(a, pc.g);
             if (row0 >= rows) continue;
-            const int na = min(NH, (rows - row0 + kRows - 1) / kRows);
+            const int na = min(NH, (rows - row0 + kRows - 1) / kRows), units = pc.u1 - pc.u0;
             if (half >= na) {
-                it += pc.u1 - pc.u0;
-                job += (pc.u1 - pc.u0) * na;
+                it += units;
+                job += units * na;
                 continue;
             }
             const int hrow0 = row0 + half * kRows, row = hrow0 + th, b = pc.g.b;
@@ -313,16 +414,16 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, NH == 1 ? 2 : 1)
             float m = -INFINITY, l = 0.f;
             job += half;
             for (int u = pc.u1 - 1; u >= pc.u0; --u, ++it, job += na, ++pv) {
-                const int s = it % NS, buf = job % SB;
                 const bool ctx = u < pc.g.ctx_units;
-                wait_on(&info_full[s], it / NS);
-                const TileInfo &ti = info[s];
+                if (ok) ok = wait_for(published, it);
+                const TileInfo &ti = info[it % NI];
                 const bool manual = ok && ti.manual;
                 const int j0 = ctx ? 0 : (u - pc.g.ctx_units) * kUnit;  // first new token
                 uint64_t sees = ~0ull;  // this row's keys of the unit
-                if (manual && half == 0) {
+                if (manual && half == 0 && (ok = wait_for(v_slots, it))) {
                     constexpr int kChunks = D / 8;
-                    uint8_t *kt = smem + L::kKv + s * 2 * L::kTile;
+                    uint8_t *kt = smem + L::kKv + (it % NK) * L::kTile;
+                    uint8_t *vt = smem + L::kVAt + (it % NV) * L::kTile;
                     const char *kn = static_cast<const char *>(a.k.p) + 2 * (b * a.k.sb + pc.hk * a.k.sh);
                     const char *vn = static_cast<const char *>(a.v.p) + 2 * (b * a.v.sb + pc.hk * a.v.sh);
 #pragma unroll 4
@@ -346,12 +447,12 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, NH == 1 ? 2 : 1)
                                                c * 16);
                             }
                         }
-                        uint8_t *d = kt + (c >> 3) * (kUnit * 128) + j * 128 + (((c & 7) ^ (j & 7)) << 4);
-                        *reinterpret_cast<uint4 *>(d) = x;
-                        *reinterpret_cast<uint4 *>(d + L::kTile) = y;
+                        const int at = (c >> 3) * (kUnit * 128) + j * 128 + (((c & 7) ^ (j & 7)) << 4);
+                        *reinterpret_cast<uint4 *>(kt + at) = x;
+                        *reinterpret_cast<uint4 *>(vt + at) = y;
                     }
                     fence_proxy_async_smem();
-                    mbar_arrive(&filled[s]);
+                    mbar_arrive(&filled[it % NI]);
                 }
                 if (manual) {
                     sees = 0;
@@ -368,8 +469,20 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, NH == 1 ? 2 : 1)
                         const int nv = min(kUnit, pc.g.n - j0);
                         if (a.tree) {
                             const uint8_t *tr = a.tree + ((size_t)b * a.T + t) * a.T + j0;
+                            if ((reinterpret_cast<uintptr_t>(tr) & 3) == 0) {
+                                // the row's bytes by fours; those behind nv are not read
+#pragma unroll
+                                for (int j = 0; j < kUnit; j += 4) {
+                                    if (j + 4 <= nv) {
+                                        const uint32_t x = __vcmpne4(*reinterpret_cast<const uint32_t *>(tr + j), 0);
+                                        sees |= (uint64_t)((x & 1) | (x >> 7 & 2) | (x >> 14 & 4) | (x >> 21 & 8)) << j;
+                                    }
+                                }
+                                for (int j = nv & ~3; j < nv; ++j) sees |= (uint64_t)(tr[j] != 0) << j;
+                            } else {
 #pragma unroll 8
-                            for (int j = 0; j < nv; ++j) sees |= (uint64_t)(tr[j] != 0) << j;
+                                for (int j = 0; j < nv; ++j) sees |= (uint64_t)(tr[j] != 0) << j;
+                            }
                         } else {
                             const int nk = min(nv, max(0, t - j0 + 1));
                             sees = nk >= 64 ? ~0ull : (1ull << nk) - 1;
@@ -380,26 +493,24 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, NH == 1 ? 2 : 1)
 #pragma unroll
                 for (int e = 0; e < kEnt; ++e)
                     sh[e] = a.w && ctx ? ti.ent[page >= kUnit ? 0 : (e * 16) >> shift].shift : 0.f;
-                wait_on(&s_full[2 * half + (pv & 1)], pv >> 1);
+                wait_on(&s_full[4 * half + (pv & 3)], pv >> 2);
                 tc_fence_after();
-                const uint32_t st = tmem + lanes + buf * kUnit;
+                const uint32_t st = tmem + lanes + (job % SB) * kUnit;
                 if (warp_live) {
                     uint32_t x0[32], x1[32];
                     tmem_ld32(st, x0);
                     tmem_ld32(st + 32, x1);
                     tmem_wait_ld();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_free[job % SB]);
                     auto at = [&](int j) -> uint32_t & { return j < 32 ? x0[j] : x1[j - 32]; };
-                    // in units of the scaled base-2 logit
-                    if (manual || a.w) {
+                    if (manual || a.w) {  // weights as a shift of the raw logit; -inf where not seen
 #pragma unroll
                         for (int j = 0; j < kUnit; ++j) {
-                            const float v = fmaf(__uint_as_float(at(j)), a.scale_log2, sh[j >> 4]);
+                            const float v = fmaf(sh[j >> 4], inv_scale, __uint_as_float(at(j)));
                             at(j) = __float_as_uint(sees >> j & 1 ? v : -INFINITY);
                         }
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < kUnit; ++j)
-                            at(j) = __float_as_uint(__uint_as_float(at(j)) * a.scale_log2);
                     }
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -407,43 +518,51 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, NH == 1 ? 2 : 1)
 #pragma unroll
                         for (int y = 0; y < 4; ++y)
                             mx[y] = fmax3(mx[y], __uint_as_float(at(j + 2 * y)), __uint_as_float(at(j + 2 * y + 1)));
-                    const float mt = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]);
+                    const float mt = fmax3(fmaxf(mx[0], mx[1]), mx[2], mx[3]) * a.scale_log2;
+                    // this half's earlier products are done: P is free, and O may be scaled
+                    if (pv > 0) wait_on(&pv_done[half], pv - 1);
                     if (__any_sync(~0u, mt > m + kLazy)) {
                         const float mn = fmaxf(m, mt);
                         const float f = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
                         m = mn;
                         l *= f;
                         if (u != pc.u1 - 1) {  // the accumulator holds this piece's earlier units
-                            wait_on(&pv_done[half], pv - 1);
                             tc_fence_after();
 #pragma unroll 1
-                            for (int ch = 0; ch < D / 32; ++ch) {
-                                uint32_t o[32];
-                                tmem_ld32(acc + ch * 32, o);
+                            for (int ch = 0; ch < D / 16; ++ch) {
+                                uint32_t o[16];
+                                tmem_ld16(acc + ch * 16, o);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                                tmem_st32(acc + ch * 32, o);
+                                for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                                tmem_st16(acc + ch * 16, o);
                             }
                             tmem_wait_st();
                         }
                     }
-                    const float mb = m == -INFINITY ? 0.f : m - E::kBias;
+                    const float mb = m == -INFINITY ? 0.f : E::kBias - m;
                     float ls[4] = {0.f, 0.f, 0.f, 0.f};
-                    uint32_t p[32];
 #pragma unroll
-                    for (int j = 0; j < kUnit; j += 2) {
-                        const float p0 = fast_exp2(__uint_as_float(at(j)) - mb);
-                        const float p1 = fast_exp2(__uint_as_float(at(j + 1)) - mb);
-                        ls[(j >> 1) & 3] += p0 + p1;
-                        p[j >> 1] = E::pack(p0, p1);  // rounded for the second product, the sum is not
+                    for (int c = 0; c < 8; ++c) {  // eight keys: one 16-byte chunk of the row
+                        uint32_t p[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float p0 = fast_exp2(fmaf(__uint_as_float(at(8 * c + 2 * j)), a.scale_log2, mb));
+                            const float p1 = fast_exp2(fmaf(__uint_as_float(at(8 * c + 2 * j + 1)), a.scale_log2, mb));
+                            ls[j] += p0 + p1;
+                            p[j] = E::pack(p0, p1);  // rounded for the second product, the sum is not
+                        }
+                        *reinterpret_cast<uint4 *>(prow + ((c ^ (th & 7)) << 4)) = make_uint4(p[0], p[1], p[2], p[3]);
                     }
                     l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
-                    tmem_st32(st, p);
-                    tmem_wait_st();
+                    fence_proxy_async_smem();
+                } else {
+                    if (lane == 0) mbar_arrive(&s_free[job % SB]);
+                    if (pv > 0) wait_on(&pv_done[half], pv - 1);
                 }
                 tc_fence_before();
-                mbar_arrive(&p_full[buf]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_full[half]);
             }
             // ---- the piece's end: rows out, or into the workspace
             job -= half;
@@ -456,14 +575,16 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, NH == 1 ? 2 : 1)
                 if (pc.u1 == pc.g.units) a.info[item].y = cta;
             }
             const size_t slot = ((size_t)rt * nct + cta) * 2 + (pc.u0 == 0 ? 1 : 0);
+            const size_t prt = slot * (NH * kRows) + half * kRows + th;  // row of the workspace
             const size_t orow = ((size_t)b * a.c.Hk * a.G + h) * a.T + t;
             const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
             if (live) {
                 if (!whole)
-                    a.part_ml[slot * (NH * kRows) + tid] = make_float2(m, l);
+                    a.part_ml[prt] = make_float2(m, l);
                 else if (a.lse)
                     a.lse[orow] = l == 0.f ? -INFINITY : (m - E::kBias + log2f(l)) * kLn2;
             }
+            __syncwarp();
             if (warp_live) {
 #pragma unroll 1
                 for (int ch = 0; ch < D / 32; ++ch) {
@@ -475,8 +596,7 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, NH == 1 ? 2 : 1)
                         for (int j = 0; j < 32; ++j)
                             o[j] = __float_as_uint(l == 0.f ? 0.f : __uint_as_float(o[j]) * inv);
                         if (!whole || a.out_f32) {
-                            float *d = whole ? static_cast<float *>(a.out) + orow * D
-                                             : a.part + (slot * (NH * kRows) + tid) * D;
+                            float *d = whole ? static_cast<float *>(a.out) + orow * D : a.part + prt * D;
                             uint4 *v = reinterpret_cast<uint4 *>(d + ch * 32);
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
@@ -497,7 +617,7 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, NH == 1 ? 2 : 1)
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == L::kWarpMma) {
+    if (warp == L::kWarpS) {
         tc_fence_after();
         tmem_dealloc(tmem, L::kTmemCols);
     }
