@@ -12,9 +12,8 @@
 // Units whose 64 keys all exist come by TMA through a map over (d, row, head, page): the page's
 // number is a coordinate, so any strides and page sizes do, and pages of 16 and 32 tokens are 4
 // and 2 boxes of one tile. The others (a sequence's last keys, the new tokens, a tile with an
-// absent page) are written by the first half's threads themselves, with zeros where no key is,
-// in the same swizzle; a run is walked from its end, so that this happens while the first
-// copies are on their way.
+// absent page) are written by the copying warps' own lanes, with zeros where no key is, in the
+// same swizzle.
 #include <cstdint>
 
 #include "cache_common.cuh"
@@ -30,7 +29,7 @@ constexpr int kEnt = 4;                    // page slots of a unit, at most (16-
 
 struct TileInfo {
     Staged ent[kEnt];
-    int manual;  // the first half's threads write this unit's tiles
+    int partial;  // some of the unit's keys do not exist
 };
 
 // NH halves. Tensor memory: kSBufs S buffers of 64 columns, then NH accumulators of D.
@@ -63,13 +62,12 @@ struct TileSmem {
     static_assert(kK >= 2 && kK + 4 + 2 <= kInfos, "ring");
     static constexpr int kInfo = kKv + kSlots * kTile;
     static constexpr int kBars = (kInfo + kInfos * (int)sizeof(TileInfo) + 7) / 8 * 8;
-    // filled [kInfos], kv_full, kv_empty [kSlots], s_free [kSBufs], s_full [NH][4], p_full,
+    // k_full, v_full, k_empty, v_empty [kSlots], s_free [kSBufs], s_full [NH][4], p_full,
     // q_full, pv_done [NH], drain [2]. A parity wait is exact for a waiter that sees every phase:
     // s_full (its units in turn) and pv_done belong to a half, the others to one of the
-    // four warps, which waits for every use in turn. Units published are counted instead: a
-    // half without rows in a piece does not follow it.
-    static constexpr int kNumBars = kInfos + 2 * kSlots + kSBufs + 7 * NH + 2;
-    static constexpr int kMisc = kBars + kNumBars * 8;  // tensor memory address, counts, abort flag
+    // four warps, which waits for every use in turn.
+    static constexpr int kNumBars = 2 * kSlots + kSBufs + 7 * NH + 2;
+    static constexpr int kMisc = kBars + kNumBars * 8;  // tensor memory address, abort flag
     static constexpr int kRun = kMisc + 16;
     static constexpr int kBytes = kRun + (int)sizeof(RunSmem);
     static constexpr int kAlloc = kBytes + 1024;
@@ -84,35 +82,6 @@ __device__ __forceinline__ void tma_load_4d(void *smem_dst, const void *tmap, ui
         " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(smem_dst)),
         "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
         : "memory");
-}
-
-__device__ __forceinline__ void store_release(int *p, int v)
-{
-    asm volatile("st.release.cta.shared::cta.s32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
-}
-
-__device__ __forceinline__ int load_acquire(const int *p)
-{
-    int v;
-    asm volatile("ld.acquire.cta.shared::cta.s32 %0, [%1];" : "=r"(v) : "r"(smem_u32(p)) : "memory");
-    return v;
-}
-
-// Wait until *p is above n; gives up as mbar_wait does.
-__device__ __forceinline__ bool wait_count(int *p, int n, volatile int *abort, int *flag)
-{
-    const uint64_t t0 = global_timer_ns();
-    for (uint32_t spin = 0;; ++spin) {
-        if (load_acquire(p) > n) return true;
-        if ((spin & 63u) == 63u) {
-            if (*abort) return false;
-            if (global_timer_ns() - t0 > kWaitLimitNs) {
-                *abort = 1;
-                raise_flag(flag, AB_FLAG_TIMEOUT);
-                return false;
-            }
-        }
-    }
 }
 
 template <typename E>
@@ -131,22 +100,18 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t *smem = align_smem_1024(smem_raw);
     TileInfo *info = reinterpret_cast<TileInfo *>(smem + L::kInfo);
-    uint64_t *filled = reinterpret_cast<uint64_t *>(smem + L::kBars);  // tiles by the softmax threads
-    uint64_t *k_full = filled + NI, *v_full = k_full + NK;  // a tile copied by TMA
+    uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + L::kBars), *v_full = k_full + NK;
     uint64_t *k_empty = v_full + NV, *v_empty = k_empty + NK, *s_free = v_empty + NV, *s_full = s_free + SB;
     uint64_t *p_full = s_full + 4 * NH, *q_full = p_full + NH, *pv_done = q_full + NH;
     uint64_t *drain = pv_done + NH;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMisc);
-    int *published = reinterpret_cast<int *>(smem + L::kMisc + 4);  // units whose info and K slot are there
-    int *v_slots = reinterpret_cast<int *>(smem + L::kMisc + 8);    // units whose V slot is free
-    volatile int *abort = reinterpret_cast<volatile int *>(smem + L::kMisc + 12);
+    volatile int *abort = reinterpret_cast<volatile int *>(smem + L::kMisc + 8);
     RunSmem &run_sm = *reinterpret_cast<RunSmem *>(smem + L::kRun);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = blockIdx.x, nct = gridDim.x, rt = blockIdx.y, row0 = rt * NH * kRows;
     const int page = a.c.page, shift = a.page_shift;
 
     if (tid == 0) {
-        for (int i = 0; i < NI; ++i) mbar_init(&filled[i], 128);
         for (int s = 0; s < L::kSlots; ++s) {
             mbar_init(&k_full[s], 1);   // and v_full behind it
             mbar_init(&k_empty[s], 1);  // and v_empty
@@ -161,8 +126,6 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
         mbar_init(&drain[0], 1);
         mbar_init(&drain[1], 1);
         *abort = 0;
-        *published = 0;
-        *v_slots = 0;
         fence_barrier_init();
     }
     if (warp == L::kWarpS) {
@@ -180,10 +143,6 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
     auto wait = [&](uint64_t *bar, uint32_t phase) -> bool {
         return __all_sync(~0u, mbar_wait(bar, phase & 1, abort, a.flag));
     };
-    auto wait_for = [&](int *count, int unit) -> bool {
-        return __all_sync(~0u, wait_count(count, unit, abort, a.flag));
-    };
-
     if (warp == L::kWarpK || warp == L::kWarpV) {
         const bool is_k = warp == L::kWarpK;
         const CUtensorMap *tm = is_k ? &tmK : &tmV;
@@ -198,7 +157,7 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
         const int batch = 32 / nent;
         int it = 0, s = 0;                  // units so far, their ring slot
         uint32_t par_e = 1;                 // parity of the slots' last release
-        uint32_t phase = 0, loaded = 0;     // bit s: parity of slot s's next copy; its last use was a copy
+        uint32_t phase = 0, loaded = 0;     // bit s: parity of slot s's next tile; its last one was copied
         bool ok = true;
         while (ok && next_piece(a, run, nct, pc, nullptr)) {
             if (row0 >= group_rows(a, pc.g)) continue;
@@ -221,31 +180,55 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
                 e.shift = __shfl_sync(~0u, eb.shift, from);
                 const int r0 = page > kUnit ? (u * kUnit) & (page - 1) : 0;
                 const bool clean = lane >= nent || (e.page >= 0 && e.valid >= r0 + box_rows);
-                const bool manual = !__all_sync(~0u, clean);
+                const bool ctx = u < pc.g.ctx_units, whole = __all_sync(~0u, clean);
                 if (it >= ns) ok = wait(&empty[s], par_e);
                 if (!ok) break;
                 if (is_k) {
                     TileInfo &ti = info[it % NI];
                     if (lane < nent) ti.ent[lane] = e;
-                    if (lane == 0) ti.manual = manual;
-                    __syncwarp();
+                    if (lane == 0) ti.partial = !whole;
                 }
-                if (lane == 0) store_release(is_k ? published : v_slots, it + 1);
-                if (manual) {
-                    loaded &= ~(1u << s);
-                } else {
+                uint8_t *tile = ring + s * L::kTile;
+                if (whole) {
+                    __syncwarp();  // the info is written before the barrier is armed
                     if (lane == 0) mbar_arrive_expect_tx(&full[s], L::kTile);
                     __syncwarp();
                     loaded |= 1u << s;
-                    phase ^= 1u << s;
                     if (lane < nent) {
-                        uint8_t *d = ring + s * L::kTile + lane * box_rows * 128;
 #pragma unroll
                         for (int y = 0; y < L::kBoxes; ++y)
-                            tma_load_4d(d + y * (kUnit * 128), tm, &full[s], y * 64, r0, pc.hk, e.page);
+                            tma_load_4d(tile + lane * box_rows * 128 + y * (kUnit * 128), tm, &full[s], y * 64, r0,
+                                        pc.hk, e.page);
                     }
+                } else {
+                    loaded &= ~(1u << s);
+                    constexpr int kChunks = D / 8;
+                    const ab_tokens &nt = is_k ? a.k : a.v;
+                    const char *fresh_rows = static_cast<const char *>(nt.p) + 2 * (pc.g.b * nt.sb + pc.hk * nt.sh);
+                    const char *base = static_cast<const char *>(is_k ? a.c.k : a.c.v) +
+                                       2 * pc.hk * (is_k ? a.c.k_head : a.c.v_head);
+                    const int64_t spage = is_k ? a.c.k_page : a.c.v_page, srow = is_k ? a.c.k_row : a.c.v_row;
+                    const int j0 = (u - pc.g.ctx_units) * kUnit;
+#pragma unroll 8
+                    for (int i = lane; i < kUnit * kChunks; i += 32) {
+                        const int j = i / kChunks, c = i % kChunks, en = page >= kUnit ? 0 : j >> shift;
+                        const int pg = __shfl_sync(~0u, e.page, en), valid = __shfl_sync(~0u, e.valid, en);
+                        uint4 x = make_uint4(0, 0, 0, 0);
+                        if (!ctx) {
+                            if (j0 + j < pc.g.n) x = ldg_stream(fresh_rows + 2 * (j0 + j) * nt.st + c * 16);
+                        } else {
+                            const int r = (u * kUnit + j) & (page - 1);
+                            if (pg >= 0 && r < valid) x = ldg_stream(base + 2 * (pg * spage + r * srow) + c * 16);
+                        }
+                        *reinterpret_cast<uint4 *>(tile + (c >> 3) * (kUnit * 128) + j * 128 +
+                                                   (((c & 7) ^ (j & 7)) << 4)) = x;
+                    }
+                    fence_proxy_async_smem();
                     __syncwarp();
+                    if (lane == 0) mbar_arrive(&full[s]);
                 }
+                phase ^= 1u << s;
+                __syncwarp();
                 if (++s == ns) {
                     s = 0;
                     par_e ^= 1;
@@ -260,10 +243,9 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
         constexpr uint32_t idesc_s = idesc<E>(kRows, kUnit, 0, 0);
         const uint64_t qd = smem_desc_sw128(smem_u32(smem), 16, 1024);
         const uint64_t kd0 = smem_desc_sw128(smem_u32(smem + L::kKv), 16, 1024);
-        int it = 0, s = 0;                // units so far, their ring slot
+        int s = 0;                        // ring slot of the next unit
         int buf = 0;                      // S buffer of the next job
-        uint32_t copied = 0;              // bit s: parity of slot s's next copy
-        uint32_t written = 0;             // bit i: parity of info slot i's next written unit
+        uint32_t tiles = 0;               // bit s: parity of slot s's next tile
         uint32_t turn = 0, phase_q = 0;   // two bits per half: its next S's barrier; bit h: its next Q
         uint32_t par_b = 1;               // parity of the S buffers' last release
         bool ok = true, used = false;     // used: every S buffer has had a job
@@ -275,17 +257,9 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
                 ok = wait(&q_full[h], phase_q >> h);
                 phase_q ^= 1u << h;
             }
-            for (int n = pc.u1 - pc.u0; ok && n > 0; --n, ++it) {
-                const int ii = it % NI;
-                ok = wait_for(published, it);
-                if (!ok) break;
-                if (info[ii].manual) {
-                    ok = wait(&filled[ii], written >> ii);
-                    written ^= 1u << ii;
-                } else {
-                    ok = wait(&k_full[s], copied >> s);
-                    copied ^= 1u << s;
-                }
+            for (int n = pc.u1 - pc.u0; ok && n > 0; --n) {
+                ok = wait(&k_full[s], tiles >> s);
+                tiles ^= 1u << s;
                 const uint64_t kd = kd0 + (uint64_t)s * (L::kTile >> 4);
                 for (int h = 0; ok && h < na; ++h) {
                     if (used) ok = wait(&s_free[buf], par_b);
@@ -322,20 +296,16 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
         constexpr uint32_t idesc_o = idesc<E>(kRows, D, 0, 1);
         const uint64_t pd = smem_desc_sw128(smem_u32(smem + L::kP), 16, 1024);
         const uint64_t vd0 = smem_desc_sw128(smem_u32(smem + L::kVAt), kUnit * 128, 1024);
-        int it = 0, s = 0;
-        uint32_t copied = 0, phase_p = 0;  // bit s: slot s's next copy; bit h: half h's next P
+        int s = 0;
+        uint32_t tiles = 0, phase_p = 0;  // bit s: slot s's next tile; bit h: half h's next P
         bool ok = true;
         while (ok && next_piece(a, run, nct, pc, nullptr)) {
             const int rows = group_rows(a, pc.g) - row0;
             if (rows <= 0) continue;
             const int na = min(NH, (rows + kRows - 1) / kRows);
-            for (int n = 0; ok && n < pc.u1 - pc.u0; ++n, ++it) {
-                // a unit that the threads wrote is there when its P is
-                ok = wait_for(published, it);
-                if (ok && !info[it % NI].manual) {
-                    ok = wait(&v_full[s], copied >> s);
-                    copied ^= 1u << s;
-                }
+            for (int n = 0; ok && n < pc.u1 - pc.u0; ++n) {
+                ok = wait(&v_full[s], tiles >> s);
+                tiles ^= 1u << s;
                 const uint64_t vd = vd0 + (uint64_t)s * (L::kTile >> 4);
                 for (int h = 0; ok && h < na; ++h) {
                     ok = wait(&p_full[h], phase_p >> h);
@@ -415,86 +385,48 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
             job += half;
             for (int u = pc.u1 - 1; u >= pc.u0; --u, ++it, job += na, ++pv) {
                 const bool ctx = u < pc.g.ctx_units;
-                if (ok) ok = wait_for(published, it);
-                const TileInfo &ti = info[it % NI];
-                const bool manual = ok && ti.manual;
-                const int j0 = ctx ? 0 : (u - pc.g.ctx_units) * kUnit;  // first new token
                 uint64_t sees = ~0ull;  // this row's keys of the unit
-                if (manual && half == 0 && (ok = wait_for(v_slots, it))) {
-                    constexpr int kChunks = D / 8;
-                    uint8_t *kt = smem + L::kKv + (it % NK) * L::kTile;
-                    uint8_t *vt = smem + L::kVAt + (it % NV) * L::kTile;
-                    const char *kn = static_cast<const char *>(a.k.p) + 2 * (b * a.k.sb + pc.hk * a.k.sh);
-                    const char *vn = static_cast<const char *>(a.v.p) + 2 * (b * a.v.sb + pc.hk * a.v.sh);
-#pragma unroll 4
-                    for (int i = th; i < kUnit * kChunks; i += 128) {
-                        const int j = i / kChunks, c = i % kChunks;
-                        uint4 x = make_uint4(0, 0, 0, 0), y = x;
-                        if (!ctx) {
-                            if (j0 + j < pc.g.n) {
-                                x = ldg_stream(kn + 2 * (j0 + j) * a.k.st + c * 16);
-                                y = ldg_stream(vn + 2 * (j0 + j) * a.v.st + c * 16);
-                            }
-                        } else {
-                            const Staged e = ti.ent[page >= kUnit ? 0 : j >> shift];
-                            const int64_t r = (u * kUnit + j) & (page - 1);
-                            if (e.page >= 0 && r < e.valid) {
-                                x = ldg_stream(static_cast<const char *>(a.c.k) +
-                                               2 * (e.page * a.c.k_page + pc.hk * a.c.k_head + r * a.c.k_row) +
-                                               c * 16);
-                                y = ldg_stream(static_cast<const char *>(a.c.v) +
-                                               2 * (e.page * a.c.v_page + pc.hk * a.c.v_head + r * a.c.v_row) +
-                                               c * 16);
-                            }
-                        }
-                        const int at = (c >> 3) * (kUnit * 128) + j * 128 + (((c & 7) ^ (j & 7)) << 4);
-                        *reinterpret_cast<uint4 *>(kt + at) = x;
-                        *reinterpret_cast<uint4 *>(vt + at) = y;
-                    }
-                    fence_proxy_async_smem();
-                    mbar_arrive(&filled[it % NI]);
-                }
-                if (manual) {
+                bool masked = false;
+                if (!ctx) {
+                    masked = true;
                     sees = 0;
-                    if (ctx) {
-#pragma unroll
-                        for (int e = 0; e < kEnt; ++e) {
-                            // keys e * 16 .. e * 16 + 15 lie in one page
-                            const Staged x = ti.ent[page >= kUnit ? 0 : (e * 16) >> shift];
-                            const int r = (u * kUnit + e * 16) & (page - 1);
-                            const int nv = x.page >= 0 ? min(16, max(0, x.valid - r)) : 0;
-                            sees |= (uint64_t)((1u << nv) - 1) << (16 * e);
-                        }
+                    const int j0 = (u - pc.g.ctx_units) * kUnit, nv = min(kUnit, pc.g.n - j0);
+                    if (live && !a.tree) {
+                        const int nk = min(nv, max(0, t - j0 + 1));
+                        sees = nk >= 64 ? ~0ull : (1ull << nk) - 1;
                     } else if (live) {
-                        const int nv = min(kUnit, pc.g.n - j0);
-                        if (a.tree) {
-                            const uint8_t *tr = a.tree + ((size_t)b * a.T + t) * a.T + j0;
-                            if ((reinterpret_cast<uintptr_t>(tr) & 3) == 0) {
-                                // the row's bytes by fours; those behind nv are not read
-#pragma unroll
-                                for (int j = 0; j < kUnit; j += 4) {
-                                    if (j + 4 <= nv) {
-                                        const uint32_t x = __vcmpne4(*reinterpret_cast<const uint32_t *>(tr + j), 0);
-                                        sees |= (uint64_t)((x & 1) | (x >> 7 & 2) | (x >> 14 & 4) | (x >> 21 & 8)) << j;
-                                    }
-                                }
-                                for (int j = nv & ~3; j < nv; ++j) sees |= (uint64_t)(tr[j] != 0) << j;
-                            } else {
-#pragma unroll 8
-                                for (int j = 0; j < nv; ++j) sees |= (uint64_t)(tr[j] != 0) << j;
+                        const uint8_t *tr = a.tree + ((size_t)b * a.T + t) * a.T + j0;
+                        int j = 0;
+                        if ((reinterpret_cast<uintptr_t>(tr) & 3) == 0) {  // four bytes at a time
+#pragma unroll 4
+                            for (; j + 4 <= nv; j += 4) {
+                                const uint32_t x = __vcmpne4(*reinterpret_cast<const uint32_t *>(tr + j), 0);
+                                sees |= (uint64_t)((x & 1) | (x >> 7 & 2) | (x >> 14 & 4) | (x >> 21 & 8)) << j;
                             }
-                        } else {
-                            const int nk = min(nv, max(0, t - j0 + 1));
-                            sees = nk >= 64 ? ~0ull : (1ull << nk) - 1;
                         }
+#pragma unroll 4
+                        for (; j < nv; ++j) sees |= (uint64_t)(tr[j] != 0) << j;
                     }
+                    __syncwarp();
                 }
-                float sh[kEnt];
-#pragma unroll
-                for (int e = 0; e < kEnt; ++e)
-                    sh[e] = a.w && ctx ? ti.ent[page >= kUnit ? 0 : (e * 16) >> shift].shift : 0.f;
                 wait_on(&s_full[4 * half + (pv & 3)], pv >> 2);
                 tc_fence_after();
+                // the unit's info was written before its keys were announced to the S warp
+                const TileInfo &ti = info[it % NI];
+                float sh[kEnt] = {0.f, 0.f, 0.f, 0.f};
+                if (ctx && (ti.partial || a.w)) {
+                    masked = true;
+                    sees = 0;
+#pragma unroll
+                    for (int e = 0; e < kEnt; ++e) {
+                        // keys e * 16 .. e * 16 + 15 lie in one page
+                        const Staged x = ti.ent[page >= kUnit ? 0 : (e * 16) >> shift];
+                        const int r = (u * kUnit + e * 16) & (page - 1);
+                        const int nv = x.page >= 0 ? min(16, max(0, x.valid - r)) : 0;
+                        sees |= (uint64_t)((1u << nv) - 1) << (16 * e);
+                        sh[e] = x.shift;
+                    }
+                }
                 const uint32_t st = tmem + lanes + (job % SB) * kUnit;
                 if (warp_live) {
                     uint32_t x0[32], x1[32];
@@ -505,7 +437,7 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s_free[job % SB]);
                     auto at = [&](int j) -> uint32_t & { return j < 32 ? x0[j] : x1[j - 32]; };
-                    if (manual || a.w) {  // weights as a shift of the raw logit; -inf where not seen
+                    if (masked) {  // weights as a shift of the raw logit; -inf where not seen
 #pragma unroll
                         for (int j = 0; j < kUnit; ++j) {
                             const float v = fmaf(sh[j >> 4], inv_scale, __uint_as_float(at(j)));
