@@ -294,28 +294,28 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const ScoreAr
 // ---------------------------------------------------------------------------------
 // ab_cache_keep: a radix selection of the budget-th largest score (three digits of the
 // fp32 bits, which order as the values do for values >= 0), then one ordered pass that
-// ranks holes and movers. A cluster takes one (sequence, key head): its CTAs hold the keys
-// of their slots in shared memory, so scores and positions are read once.
+// ranks holes and movers. Bound by one read of scores and positions (8 bytes per slot); its
+// CTAs hold the keys of their slots in shared memory, so that happens once. One CTA takes a
+// (sequence, key head) of up to 16384 slots; longer ones take a cluster of CTAs that add
+// their histograms through distributed shared memory (a cluster of two for 4160 slots cost
+// 50 us for 256 heads, its barriers and remote reads, against {KEEP_US} us in one CTA).
 // ---------------------------------------------------------------------------------
-constexpr int kKeepThreads = 512;
 constexpr int kKeepBins = 2048;
 constexpr int kKeepSmem = 45 * 1024;  // keys of one CTA held in shared memory (180 KB)
 
-__device__ __forceinline__ uint32_t keep_key(const CacheKeep &a, int b, int hk, int slot, int limit)
+// The key of a slot at index `at` of score and pos: order of the score, +inf when recent.
+__device__ __forceinline__ uint32_t keep_key(float x, int pos, int recent, int limit, int *flag)
 {
-    const int page = a.c.page, pg = cache_page(a.c, b, slot / page, a.flag);
-    if (pg < 0) return 0;
-    const size_t at = ((size_t)pg * a.c.Hk + hk) * page + slot % page;
-    if (a.recent > 0 && a.pos[at] >= limit) return 0x7f800000u;
-    const float x = a.score[at];
+    if (recent > 0 && pos >= limit) return 0x7f800000u;
     if (!(x >= 0.f)) {
-        raise_flag(a.flag, AB_FLAG_BAD_SCORE);
+        raise_flag(flag, AB_FLAG_BAD_SCORE);
         return 0;
     }
     return __float_as_uint(x) & 0x7fffffffu;  // -0 counts as 0
 }
 
-// Sum of x over the threads before this one, and over all (block of kKeepThreads).
+// Sum of x over the threads before this one, and over all.
+template <int kThreads>
 __device__ __forceinline__ int block_scan(int x, int *sm_warp, int *total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -328,207 +328,277 @@ __device__ __forceinline__ int block_scan(int x, int *sm_warp, int *total)
     __syncthreads();
     if (lane == 31) sm_warp[warp] = incl;
     __syncthreads();
-    int before = 0, all = 0;
+    // every warp scans the warps' sums
+    const int mine = lane < kThreads / 32 ? sm_warp[lane] : 0;
+    int w = mine;
 #pragma unroll
-    for (int w = 0; w < kKeepThreads / 32; ++w) {
-        const int v = sm_warp[w];
-        if (w < warp) before += v;
-        all += v;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(~0u, w, o);
+        if (lane >= o) w += y;
     }
-    *total = all;
-    return before + incl - x;
+    *total = __shfl_sync(~0u, w, 31);
+    return __shfl_sync(~0u, w - mine, warp) + incl - x;
 }
 
-__global__ void __launch_bounds__(kKeepThreads) cache_keep_kernel(const CacheKeep a, int held)
+template <bool kCluster, int kThreads>
+__global__ void __launch_bounds__(kThreads) cache_keep_kernel(const CacheKeep a, int held, int page_shift)
 {
-    extern __shared__ __align__(16) uint32_t keys[];  // [held]
+    extern __shared__ __align__(16) uint32_t keys[];  // [held]: keys, later the slots' sources
     __shared__ int hist[kKeepBins];
-    __shared__ int sm_warp[kKeepThreads / 32];
+    __shared__ int sm_warp[32];
     __shared__ int sm_digit, sm_above;
     __shared__ int3 sm_cnt;  // this CTA's keys equal to the threshold, holes, movers
     cg::cluster_group cl = cg::this_cluster();
-    const int cs = cl.num_blocks(), rank = cl.block_rank(), tid = threadIdx.x;
+    const int cs = kCluster ? cl.num_blocks() : 1, rank = kCluster ? cl.block_rank() : 0, tid = threadIdx.x;
+    auto sync = [&]() {
+        if (kCluster)
+            cl.sync();
+        else
+            __syncthreads();
+    };
     const int item = blockIdx.x / cs, hk = item % a.c.Hk, b = item / a.c.Hk;
+    const int page = a.c.page;
     const int len = cache_len(a.c, a.length, b, tid == 0 ? a.flag : nullptr);
     const int m = min(len, a.budget);
     int32_t *src = a.src + (size_t)item * a.budget;
     if (hk == 0 && rank == 0 && tid == 0) a.n_keep[b] = m;
-    for (int j = m + rank * kKeepThreads + tid; j < a.budget; j += cs * kKeepThreads) src[j] = -1;
+    for (int j = m + rank * kThreads + tid; j < a.budget; j += cs * kThreads) src[j] = -1;
     if (len <= a.budget) {
-        for (int j = rank * kKeepThreads + tid; j < m; j += cs * kKeepThreads) src[j] = j;
+        for (int j = rank * kThreads + tid; j < m; j += cs * kThreads) src[j] = j;
         return;
     }
     const int limit = a.recent > 0 ? a.next_pos[b] - a.recent : 0;
     const int sl = (len + cs - 1) / cs, s0 = min(len, rank * sl), ns = min(len, s0 + sl) - s0;
-    for (int i = tid; i < min(ns, held); i += kKeepThreads) keys[i] = keep_key(a, b, hk, s0 + i, limit);
-    auto key_of = [&](int i) { return i < held ? keys[i] : keep_key(a, b, hk, s0 + i, limit); };
+    auto index_of = [&](int i) -> int64_t {  // of slot s0 + i in score and pos, or -1
+        const int slot = s0 + i, pg = cache_page(a.c, b, slot >> page_shift, a.flag);
+        return pg < 0 ? -1 : ((int64_t)pg * a.c.Hk + hk) * page + (slot & (page - 1));
+    };
+    auto key_far = [&](int i) -> uint32_t {  // a key that is not held
+        const int64_t at = index_of(i);
+        return at < 0 ? 0 : keep_key(a.score[at], a.recent > 0 ? a.pos[at] : 0, a.recent, limit, a.flag);
+    };
+    auto key_of = [&](int i) { return i < held ? keys[i] : key_far(i); };
+    for (int i = tid; i < kKeepBins; i += kThreads) hist[i] = 0;
+    __syncthreads();
+    // four slots per thread in flight; the first digit is counted on the way
+    const int nh = min(ns, held);
+    for (int i0 = tid; i0 < nh; i0 += 4 * kThreads) {
+        int64_t at[4];
+        float x[4];
+        int p[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) at[q] = i0 + q * kThreads < nh ? index_of(i0 + q * kThreads) : -1;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            x[q] = at[q] >= 0 ? a.score[at[q]] : 0.f;
+            p[q] = at[q] >= 0 && a.recent > 0 ? a.pos[at[q]] : INT32_MIN;
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (i0 + q * kThreads >= nh) break;
+            const uint32_t k = at[q] < 0 ? 0 : keep_key(x[q], p[q], a.recent, limit, a.flag);
+            keys[i0 + q * kThreads] = k;
+            atomicAdd(&hist[k >> 20], 1);
+        }
+    }
 
     // ---- threshold: `need` keys are kept among those that share the digits found so far
     uint32_t prefix = 0, mask = 0;
     int need = m;
+    constexpr int kPer = kKeepBins / kThreads;
     for (int d = 0; d < 3; ++d) {
         const int shift = d == 0 ? 20 : d == 1 ? 9 : 0, bits = d == 2 ? 9 : 11;
-        for (int i = tid; i < kKeepBins; i += kKeepThreads) hist[i] = 0;
-        __syncthreads();
-        for (int i = tid; i < ns; i += kKeepThreads) {
+        if (d > 0) {
+            for (int i = tid; i < kKeepBins; i += kThreads) hist[i] = 0;
+            __syncthreads();
+        }
+        for (int i = (d == 0 ? nh : 0) + tid; i < ns; i += kThreads) {
             const uint32_t k = key_of(i);
             if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1);
         }
-        cl.sync();
-        // bins from the highest down, four per thread
-        int h[4], sum = 0;
+        sync();
+        // bins from the highest down, kPer per thread
+        int h[kPer], sum = 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int bin = kKeepBins - 1 - (4 * tid + j);
+        for (int j = 0; j < kPer; ++j) {
+            const int bin = kKeepBins - 1 - (kPer * tid + j);
             h[j] = 0;
-            for (int k = 0; k < cs; ++k) h[j] += cl.map_shared_rank(hist, k)[bin];
+            if (kCluster)
+                for (int k = 0; k < cs; ++k) h[j] += cl.map_shared_rank(hist, k)[bin];
+            else
+                h[j] = hist[bin];
             sum += h[j];
         }
         int total;
-        int above = block_scan(sum, sm_warp, &total);
+        int above = block_scan<kThreads>(sum, sm_warp, &total);
         if (above < need && above + sum >= need) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < kPer; ++j) {
                 if (above < need && above + h[j] >= need) {
-                    sm_digit = kKeepBins - 1 - (4 * tid + j);
+                    sm_digit = kKeepBins - 1 - (kPer * tid + j);
                     sm_above = above;
                     break;
                 }
                 above += h[j];
             }
         }
-        cl.sync();  // the histograms are read; the digit is visible
+        sync();  // the histograms are read; the digit is visible
         prefix |= (uint32_t)sm_digit << shift;
         mask |= ((1u << bits) - 1) << shift;
         need -= sm_above;
         __syncthreads();
     }
 
-    // ---- one ordered pass: thread t takes the slots [t per, (t + 1) per) of the CTA
-    const int per = (ns + kKeepThreads - 1) / kKeepThreads;
+    // ---- one ordered pass: thread t takes the slots [t per, (t + 1) per) of the CTA (an odd
+    // number, so that the threads' shared memory reads fall into different banks)
+    const int per = ((ns + kThreads - 1) / kThreads) | 1;
     const int i0 = min(ns, tid * per), i1 = min(ns, i0 + per);
     int eq = 0;
     for (int i = i0; i < i1; ++i) eq += key_of(i) == prefix;
     int total;
-    int eq_rank = block_scan(eq, sm_warp, &total);
-    if (tid == 0) sm_cnt.x = total;
-    cl.sync();
-    for (int k = 0; k < rank; ++k) eq_rank += cl.map_shared_rank(&sm_cnt, k)->x;
+    int eq_rank = block_scan<kThreads>(eq, sm_warp, &total);
+    if (kCluster) {
+        if (tid == 0) sm_cnt.x = total;
+        cl.sync();
+        for (int k = 0; k < rank; ++k) eq_rank += cl.map_shared_rank(&sm_cnt, k)->x;
+    }
     int holes = 0, movers = 0, e = eq_rank;
     for (int i = i0; i < i1; ++i) {
         const uint32_t k = key_of(i);
         const bool kept = k > prefix || (k == prefix && e < need);
         e += k == prefix;
-        const int s = s0 + i;
-        if (s < m) {
-            if (kept)
-                src[s] = s;
-            else
-                ++holes;
-        } else {
+        if (s0 + i < m)
+            holes += !kept;
+        else
             movers += kept;
+    }
+    int hole_rank = block_scan<kThreads>(holes, sm_warp, &total);
+    if (kCluster && tid == 0) sm_cnt.y = total;
+    int mover_rank = block_scan<kThreads>(movers, sm_warp, &total);
+    if (kCluster) {
+        if (tid == 0) sm_cnt.z = total;
+        cl.sync();
+        for (int k = 0; k < rank; ++k) {
+            const int3 *o = cl.map_shared_rank(&sm_cnt, k);
+            hole_rank += o->y;
+            mover_rank += o->z;
         }
     }
-    int hole_rank = block_scan(holes, sm_warp, &total);
-    if (tid == 0) sm_cnt.y = total;
-    int mover_rank = block_scan(movers, sm_warp, &total);
-    if (tid == 0) sm_cnt.z = total;
-    cl.sync();
-    for (int k = 0; k < rank; ++k) {
-        const int3 *o = cl.map_shared_rank(&sm_cnt, k);
-        hole_rank += o->y;
-        mover_rank += o->z;
-    }
+    // the movers' slots by rank; a held slot below m keeps its own number, or its rank among
+    // the holes, in place of its key
     int32_t *mv = a.movers + (size_t)item * a.budget;
-    if (movers) {
-        e = eq_rank;
-        for (int i = i0; i < i1; ++i) {
-            const uint32_t k = key_of(i);
-            const bool kept = k > prefix || (k == prefix && e < need);
-            e += k == prefix;
-            if (kept && s0 + i >= m) mv[mover_rank++] = s0 + i;
+    e = eq_rank;
+    for (int i = i0; i < i1; ++i) {
+        const uint32_t k = key_of(i);
+        const bool kept = k > prefix || (k == prefix && e < need);
+        e += k == prefix;
+        const int s = s0 + i;
+        if (s >= m) {
+            if (kept) mv[mover_rank++] = s;
+        } else if (i < held) {
+            keys[i] = kept ? (uint32_t)s : 0x80000000u | hole_rank;
+            hole_rank += !kept;
+        } else {
+            src[s] = kept ? s : -1 - hole_rank;
+            hole_rank += !kept;
         }
     }
     __threadfence();
-    cl.sync();
-    if (holes) {
-        e = eq_rank;
-        for (int i = i0; i < i1 && s0 + i < m; ++i) {
-            const uint32_t k = key_of(i);
-            const bool kept = k > prefix || (k == prefix && e < need);
-            e += k == prefix;
-            if (!kept) src[s0 + i] = __ldcg(mv + hole_rank++);
+    sync();
+    for (int i = tid; i < ns && s0 + i < m; i += kThreads) {
+        const int s = s0 + i;
+        if (i < held) {
+            const uint32_t k = keys[i];
+            src[s] = k & 0x80000000u ? __ldcg(mv + (k & 0x7fffffffu)) : (int)k;
+        } else {
+            const int k = __ldcg(src + s);
+            if (k < 0) src[s] = __ldcg(mv + (-1 - k));
         }
     }
 }
 
 // ---------------------------------------------------------------------------------
 // ab_cache_compact: one CTA per (page below the budget, key head, sequence). Rows move from
-// slots >= n_keep to slots < n_keep only, so no CTA writes what another one reads.
+// slots >= n_keep to slots < n_keep only, so no CTA writes what another one reads. A page
+// that changed is read whole for its sum. Bound by the moved rows (read and written once) and
+// those sums; the first threads look the rows' sources up, so that every row's loads are
+// independent.
 // ---------------------------------------------------------------------------------
 template <typename E, int D>
-__global__ void __launch_bounds__(kPageThreads)
-    cache_compact_kernel(const ab_cache c, int budget, const int32_t *src_all, const int32_t *n_keep, int *flag)
+__global__ void __launch_bounds__(kPageThreads, 10)
+    cache_compact_kernel(const ab_cache c, int budget, int page_shift, const int32_t *src_all,
+                         const int32_t *n_keep, int *flag)
 {
     using Sum = PageSum<D>;
     __shared__ __align__(16) float sm[Sum::kGroups * D];
-    __shared__ int sm_src[128];
+    __shared__ int sm_page[128], sm_row[128];  // pool page and row of each row's source
     const int lp = blockIdx.x, hk = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
-    const int page = c.page, cap = c.max_pages * page;
+    const int page = c.page, cap = c.max_pages << page_shift;
     const bool first = lp == 0 && hk == 0 && tid == 0;
     const int n = clamp_flag(n_keep[b], 0, min(budget, cap), first ? flag : nullptr);
     if (first) c.length[b] = n;
-    if (lp * page >= n) return;
-    const int rows = min(page, n - lp * page);
+    if (lp << page_shift >= n) return;
+    const int rows = min(page, n - (lp << page_shift));
     bool moves = false;
+    int s = 0;
+    const int j = (lp << page_shift) + tid;
     if (tid < rows) {
-        const int j = lp * page + tid;
-        int s = src_all[((size_t)b * c.Hk + hk) * budget + j];
+        s = src_all[((size_t)b * c.Hk + hk) * budget + j];
         if (s != j && (s < n || s >= cap)) {
             raise_flag(flag, AB_FLAG_BAD_INDEX);
             s = j;
         }
         moves = s != j;
-        sm_src[tid] = s;
     }
     const bool changed = __syncthreads_or(moves);
     if (!changed && rows == page) return;
     const int pg = cache_page(c, b, lp, flag);
     if (pg < 0) return;
-    const int lane = tid % Sum::kLanes;
-    char *kp = static_cast<char *>(c.k) + 2 * (pg * c.k_page + hk * c.k_head) + lane * 16;
-    char *vp = static_cast<char *>(c.v) + 2 * (pg * c.v_page + hk * c.v_head) + lane * 16;
     const size_t head = (size_t)pg * c.Hk + hk;
+    if (tid < rows) {
+        int from = moves ? cache_page(c, b, s >> page_shift, flag) : -1;
+        sm_page[tid] = from;
+        sm_row[tid] = s & (page - 1);
+        if (from >= 0) {
+            const size_t f = ((size_t)from * c.Hk + hk) * page + (s & (page - 1)), t = head * page + tid;
+            if (c.mass) c.mass[t] = c.mass[f];
+            if (c.pos) c.pos[t] = c.pos[f];
+        }
+    }
+    __syncthreads();
+    const int lane = tid % Sum::kLanes;
+    char *kc = static_cast<char *>(c.k) + 2 * hk * c.k_head + lane * 16;
+    char *vc = static_cast<char *>(c.v) + 2 * hk * c.v_head + lane * 16;
+    char *kp = kc + 2 * pg * c.k_page, *vp = vc + 2 * pg * c.v_page;
     Sum sum;
     sum.clear();
-#pragma unroll 4
-    for (int r = tid / Sum::kLanes; r < rows; r += Sum::kGroups) {
-        const int s = sm_src[r];
-        uint4 x;
-        int from = -1;
-        if (s != lp * page + r) from = cache_page(c, b, s / page, flag);
-        if (from >= 0) {
-            const int64_t fr = s % page;
-            x = ldg_stream(static_cast<const char *>(c.k) +
-                           2 * (from * c.k_page + hk * c.k_head + fr * c.k_row) + lane * 16);
-            const uint4 y = ldg_stream(static_cast<const char *>(c.v) +
-                                       2 * (from * c.v_page + hk * c.v_head + fr * c.v_row) + lane * 16);
-            *reinterpret_cast<uint4 *>(kp + 2 * r * c.k_row) = x;
-            *reinterpret_cast<uint4 *>(vp + 2 * r * c.v_row) = y;
-            if (lane == 0) {
-                const size_t f = ((size_t)from * c.Hk + hk) * page + fr, t = head * page + r;
-                if (c.mass) c.mass[t] = c.mass[f];
-                if (c.pos) c.pos[t] = c.pos[f];
-            }
-        } else if (c.ksum) {
-            x = *reinterpret_cast<const uint4 *>(kp + 2 * r * c.k_row);
-        } else {
-            continue;
+    constexpr int kBatch = 4;
+    for (int r0 = tid / Sum::kLanes; r0 < rows; r0 += kBatch * Sum::kGroups) {
+        uint4 x[kBatch], y[kBatch];
+        int from[kBatch];
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            const int r = r0 + q * Sum::kGroups;
+            from[q] = r < rows ? sm_page[r] : -1;
+            const int64_t fr = from[q] >= 0 ? sm_row[r] : r;
+            if (r < rows && (from[q] >= 0 || c.ksum))
+                x[q] = ldg_stream(from[q] >= 0 ? kc + 2 * (from[q] * c.k_page + fr * c.k_row) : kp + 2 * fr * c.k_row);
+            if (from[q] >= 0) y[q] = ldg_stream(vc + 2 * (from[q] * c.v_page + fr * c.v_row));
         }
-        sum.template add<E>(x);
+#pragma unroll
+        for (int q = 0; q < kBatch; ++q) {
+            const int64_t r = r0 + q * Sum::kGroups;
+            if (from[q] >= 0) {
+                *reinterpret_cast<uint4 *>(kp + 2 * r * c.k_row) = x[q];
+                *reinterpret_cast<uint4 *>(vp + 2 * r * c.v_row) = y[q];
+            }
+            if (r < rows) sum.template add<E>(x[q]);
+        }
     }
     if (c.ksum) sum.finish(sm, c.ksum + head * D);
 }
+
+int shift_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
 
 template <typename K, typename... A>
 cudaError_t launch_cluster(K kern, int cs, int blocks, int threads, size_t smem, cudaStream_t st, A... args)
@@ -622,12 +692,16 @@ cudaError_t launch_cache_score(const ab_cache &c, const ab_tokens &q, int G, int
 cudaError_t launch_cache_keep(const CacheKeep &a, cudaStream_t st)
 {
     const int cap = a.c.max_pages * a.c.page, items = a.c.B * a.c.Hk;
-    // a CTA per 4096 slots, up to a cluster of 8
-    int cs = 1;
-    while (cs < 8 && cap > 4096 * cs) cs *= 2;
+    const int shift = shift_of(a.c.page);
+    if (cap <= 16384)
+        return launch_cluster(cache_keep_kernel<false, 1024>, 1, items, 1024, (size_t)cap * 4, st, a, cap, shift);
+    // a CTA per 8192 slots, up to a cluster of 8 (clusters of 16 find room for few at a time:
+    // 430 us against {KEEP_PROMPT} us for 32 heads of 118800 slots)
+    int cs = 2;
+    while (cs < 8 && cap > 8192 * cs) cs *= 2;
     int held = (cap + cs - 1) / cs;
     if (held > kKeepSmem) held = kKeepSmem;
-    return launch_cluster(cache_keep_kernel, cs, items * cs, kKeepThreads, (size_t)held * 4, st, a, held);
+    return launch_cluster(cache_keep_kernel<true, 1024>, cs, items * cs, 1024, (size_t)held * 4, st, a, held, shift);
 }
 
 cudaError_t launch_cache_compact(const ab_cache &c, int budget, const int32_t *src,
@@ -636,13 +710,9 @@ cudaError_t launch_cache_compact(const ab_cache &c, int budget, const int32_t *s
     const int most = budget < c.max_pages * c.page ? budget : c.max_pages * c.page;
     const dim3 grid((most + c.page - 1) / c.page, c.Hk, c.B);
     const bool h = c.dtype == AB_F16;
-    if (c.d == 64) {
-        if (h) cache_compact_kernel<Fp16, 64><<<grid, kPageThreads, 0, st>>>(c, budget, src, n_keep, flag);
-        else cache_compact_kernel<Bf16, 64><<<grid, kPageThreads, 0, st>>>(c, budget, src, n_keep, flag);
-    } else {
-        if (h) cache_compact_kernel<Fp16, 128><<<grid, kPageThreads, 0, st>>>(c, budget, src, n_keep, flag);
-        else cache_compact_kernel<Bf16, 128><<<grid, kPageThreads, 0, st>>>(c, budget, src, n_keep, flag);
-    }
+    auto kern = c.d == 64 ? (h ? cache_compact_kernel<Fp16, 64> : cache_compact_kernel<Bf16, 64>)
+                          : (h ? cache_compact_kernel<Fp16, 128> : cache_compact_kernel<Bf16, 128>);
+    kern<<<grid, kPageThreads, 0, st>>>(c, budget, shift_of(c.page), src, n_keep, flag);
     return cudaGetLastError();
 }
 
