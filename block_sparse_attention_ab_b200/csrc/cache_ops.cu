@@ -340,8 +340,9 @@ __device__ __forceinline__ int block_scan(int x, int *sm_warp, int *total)
     return __shfl_sync(~0u, w - mine, warp) + incl - x;
 }
 
-template <bool kCluster, int kThreads>
-__global__ void __launch_bounds__(kThreads) cache_keep_kernel(const CacheKeep a, int held, int page_shift)
+// kFar: a CTA has more slots than it holds keys; those are read again in every pass.
+template <bool kCluster, bool kFar, int kThreads>
+__global__ void __launch_bounds__(kThreads, kFar ? 1 : 2) cache_keep_kernel(const CacheKeep a, int held, int page_shift)
 {
     extern __shared__ __align__(16) uint32_t keys[];  // [held]: keys, later the slots' sources
     __shared__ int hist[kKeepBins];
@@ -377,7 +378,7 @@ __global__ void __launch_bounds__(kThreads) cache_keep_kernel(const CacheKeep a,
         const int64_t at = index_of(i);
         return at < 0 ? 0 : keep_key(a.score[at], a.recent > 0 ? a.pos[at] : 0, a.recent, limit, a.flag);
     };
-    auto key_of = [&](int i) { return i < held ? keys[i] : key_far(i); };
+    auto key_of = [&](int i) { return !kFar || i < held ? keys[i] : key_far(i); };
     for (int i = tid; i < kKeepBins; i += kThreads) hist[i] = 0;
     __syncthreads();
     // four slots per thread in flight; the first digit is counted on the way
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(kThreads) cache_keep_kernel(const CacheKeep a,
             for (int i = tid; i < kKeepBins; i += kThreads) hist[i] = 0;
             __syncthreads();
         }
-        for (int i = (d == 0 ? nh : 0) + tid; i < ns; i += kThreads) {
+        for (int i = (d == 0 ? nh : 0) + tid; i < ns; i += kThreads) {  // none at first unless kFar
             const uint32_t k = key_of(i);
             if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1);
         }
@@ -495,7 +496,7 @@ __global__ void __launch_bounds__(kThreads) cache_keep_kernel(const CacheKeep a,
         const int s = s0 + i;
         if (s >= m) {
             if (kept) mv[mover_rank++] = s;
-        } else if (i < held) {
+        } else if (!kFar || i < held) {
             keys[i] = kept ? (uint32_t)s : 0x80000000u | hole_rank;
             hole_rank += !kept;
         } else {
@@ -507,7 +508,7 @@ __global__ void __launch_bounds__(kThreads) cache_keep_kernel(const CacheKeep a,
     sync();
     for (int i = tid; i < ns && s0 + i < m; i += kThreads) {
         const int s = s0 + i;
-        if (i < held) {
+        if (!kFar || i < held) {
             const uint32_t k = keys[i];
             src[s] = k & 0x80000000u ? __ldcg(mv + (k & 0x7fffffffu)) : (int)k;
         } else {
@@ -694,14 +695,15 @@ cudaError_t launch_cache_keep(const CacheKeep &a, cudaStream_t st)
     const int cap = a.c.max_pages * a.c.page, items = a.c.B * a.c.Hk;
     const int shift = shift_of(a.c.page);
     if (cap <= 16384)
-        return launch_cluster(cache_keep_kernel<false, 1024>, 1, items, 1024, (size_t)cap * 4, st, a, cap, shift);
+        return launch_cluster(cache_keep_kernel<false, false, 1024>, 1, items, 1024, (size_t)cap * 4, st, a, cap, shift);
     // a CTA per 8192 slots, up to a cluster of 8 (clusters of 16 find room for few at a time:
     // 430 us against {KEEP_PROMPT} us for 32 heads of 118800 slots)
     int cs = 2;
     while (cs < 8 && cap > 8192 * cs) cs *= 2;
     int held = (cap + cs - 1) / cs;
     if (held > kKeepSmem) held = kKeepSmem;
-    return launch_cluster(cache_keep_kernel<true, 1024>, cs, items * cs, 1024, (size_t)held * 4, st, a, held, shift);
+    auto kern = held * cs < cap ? cache_keep_kernel<true, true, 1024> : cache_keep_kernel<true, false, 1024>;
+    return launch_cluster(kern, cs, items * cs, 1024, (size_t)held * 4, st, a, held, shift);
 }
 
 cudaError_t launch_cache_compact(const ab_cache &c, int budget, const int32_t *src,

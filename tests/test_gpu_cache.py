@@ -468,6 +468,7 @@ def test_mass_many_rows_adds_up():
     ([1000, 999], 3, 64, 257, 40),
     ([5000, 4097, 4096], 1, 128, 4096, 100),
     ([40000], 1, 16, 12345, 1000),
+    ([400000, 30], 1, 16, 200001, 1000),  # more than a cluster of CTAs holds
 ])
 @pytest.mark.parametrize("ties", [False, True])
 def test_keep_and_compact(lengths, Hk, page, budget, recent, ties):
