@@ -1,4 +1,5 @@
-"""Build libab_attn.so in-tree with nvcc for sm_100a (no JIT cache, no torch build)."""
+"""Build libab_attn.so in-tree with nvcc for sm_100a (no JIT cache), and beside it _cache_bind.so,
+the compiled Python binding of the key/value cache calls (host code only, torch's headers)."""
 
 from __future__ import annotations
 
@@ -16,21 +17,48 @@ SOURCES = ["ab_api.cu", "score_kernels.cu", "select_kernels.cu", "attn_kernel.cu
 HEADERS = ["ab_device.cuh", "ab_kernels.h", "cache_common.cuh", "cache_kernels.h",
            "cache_sched.cuh", "tmap_host.h",
            os.path.join("..", "..", "include", "ab_attn.h")]
+BINDING = os.path.join(HERE, "_cache_bind.so")
+BINDING_SOURCE = "cache_bind.cpp"
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB):
+def _stale(out, sources) -> bool:
+    if not os.path.exists(out):
         return True
-    t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [__file__]
-    return any(os.path.getmtime(p) > t for p in deps)
+    t = os.path.getmtime(out)
+    return any(os.path.getmtime(p) > t for p in [os.path.join(CSRC, f) for f in sources] + [__file__])
+
+
+def build_binding() -> str:
+    """Compile _cache_bind.so against the running interpreter's torch."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    inc = [*cpp_extension.include_paths(), sysconfig.get_paths()["include"],
+           os.path.join(os.path.dirname(os.path.dirname(NVCC)), "include")]
+    tmp = BINDING + ".tmp"
+    subprocess.check_call(
+        ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+         "-DTORCH_EXTENSION_NAME=_cache_bind", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+         *(f"-I{p}" for p in inc), os.path.join(CSRC, BINDING_SOURCE), "-o", tmp, f"-L{HERE}", "-l:libab_attn.so",
+         f"-L{libs}", "-lc10", "-lc10_cuda", "-ltorch", "-ltorch_cpu", "-ltorch_python", "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, BINDING)
+    return BINDING
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
-        return LIB
+    if force or _stale(LIB, SOURCES + HEADERS):
+        _build_library(verbose)
+    if force or _stale(BINDING, [BINDING_SOURCE, HEADERS[-1]]):
+        build_binding()
+    return LIB
+
+
+def _build_library(verbose: bool) -> str:
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
     objs = []
