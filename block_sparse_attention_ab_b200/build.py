@@ -13,9 +13,10 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libab_attn.so")
 SOURCES = ["ab_api.cu", "score_kernels.cu", "select_kernels.cu", "attn_kernel.cu", "ab_noalloc.cu",
            "ab_selftest.cu", "ab_host.cu", "attn_bwd_kernel.cu", "cache_api.cu", "cache_attn.cu",
-           "cache_mass.cu", "cache_ops.cu", "cache_tiles.cu"]
+           "cache_mass.cu", "cache_mass_tiles.cu",
+           "cache_ops.cu", "cache_tiles.cu"]
 HEADERS = ["ab_device.cuh", "ab_kernels.h", "cache_common.cuh", "cache_kernels.h",
-           "cache_sched.cuh", "tmap_host.h",
+           "cache_sched.cuh", "cache_tma.cuh", "tmap_host.h",
            os.path.join("..", "..", "include", "ab_attn.h")]
 BINDING = os.path.join(HERE, "_cache_bind.so")
 BINDING_SOURCE = "cache_bind.cpp"
@@ -61,7 +62,7 @@ def build(force: bool = False, verbose: bool = False) -> str:
 def _build_library(verbose: bool) -> str:
     objdir = os.path.join(HERE, "_build")
     os.makedirs(objdir, exist_ok=True)
-    objs = []
+    objs, jobs = [], []
     for src in SOURCES:
         obj = os.path.join(objdir, src.replace(".cu", ".o"))
         cmd = [NVCC, *ARCH, "-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC",
@@ -69,8 +70,11 @@ def _build_library(verbose: bool) -> str:
                os.path.join(CSRC, src), "-o", obj]
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
-        subprocess.check_call(cmd)
+        jobs.append((cmd, subprocess.Popen(cmd)))
         objs.append(obj)
+    for cmd, job in jobs:
+        if job.wait() != 0:
+            raise subprocess.CalledProcessError(job.returncode, cmd)
     tmp = LIB + ".tmp"
     subprocess.check_call([NVCC, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs])
     os.replace(tmp, LIB)

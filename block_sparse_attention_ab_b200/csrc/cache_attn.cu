@@ -48,6 +48,7 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_attn_kernel(const CacheAt
     const int cta = blockIdx.x, nct = gridDim.x, rt = blockIdx.y;
     const int page = a.c.page, page_shift = a.page_shift;
 
+    cudaTriggerProgrammaticLaunchCompletion();  // the join may come up and wait
     Run run = find_run<kThreads>(a, sm.run, cta, nct, rt == 0 ? a.flag : nullptr);
     Piece pc;
     while (next_piece(a, run, nct, pc, rt == 0 ? a.flag : nullptr)) {
@@ -369,45 +370,58 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_attn_kernel(const CacheAt
 }
 
 // Joins the parts of rows that several CTAs computed, and writes the rows nobody computed
-// (behind n_tok, or with nothing to see). One CTA per output row; parts in CTA order.
-template <typename E, int D>
-__global__ void __launch_bounds__(128) cache_join_kernel(const CacheAttn a, int tile_rows, int nct)
+// (behind n_tok, or with nothing to see). kWarps warps share a row and take its parts in turn
+// (one warp where a row has few parts: 29 -> {JOIN} us for 20480 rows of 2 or 3 parts; four
+// where a long row is cut into many). The order of the sums depends on the parts alone.
+template <typename E, int D, int kRowWarps>
+__global__ void __launch_bounds__(128) cache_join_kernel(const CacheAttn a, int tile_rows, int nct, int rows)
 {
+    constexpr int kPer = 4 / kRowWarps;  // rows of a CTA
+    constexpr int V = D / 32;            // values per lane
     __shared__ float sm_m[4], sm_l[4], sm_o[4][D];
-    constexpr int V = D / 32;  // values per lane
-    cudaGridDependencySynchronize();
-    const int t = blockIdx.x % a.T, h = (blockIdx.x / a.T) % (a.c.Hk * a.G);
-    const int b = blockIdx.x / a.T / (a.c.Hk * a.G), hk = h / a.G;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % kRowWarps;
+    const int row = blockIdx.x * kPer + warp / kRowWarps;
+    const bool exists = row < rows;
+    const int rr = exists ? row : rows - 1;
+    const int t = rr % a.T, h = (rr / a.T) % (a.c.Hk * a.G), b = rr / a.T / (a.c.Hk * a.G), hk = h / a.G;
     const int tp = a.per_token ? t : 0;
     const int gi = a.idx ? (b * a.c.Hk + hk) * a.Tp + tp : b;
-    const Group gr = load_group(a, gi, nullptr);
-    const size_t orow = blockIdx.x;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const Group gr = load_group(a, gi, nullptr);  // inputs of the call: complete before the first kernel
     float o[V], mt = -INFINITY, lt = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) o[v] = 0.f;
-    const bool dead = t >= gr.n, empty = gr.units == 0;
-    if (!dead && !empty) {
+    const bool dead = t >= gr.n;
+    bool write = exists;
+    cudaGridDependencySynchronize();
+    if (exists && !dead && gr.units > 0) {
         const int r = a.per_token ? h % a.G : t * a.G + h % a.G;
         const int rt = r / tile_rows, n = r % tile_rows;
         int2 who = a.info[((b * a.c.Hk + hk) * a.Tp + tp) * a.row_tiles + rt];
         // inside the workspace even where a kernel gave up waiting before it wrote them
         who.x = min(max(who.x, 0), nct - 1);
         who.y = min(max(who.y, who.x), nct - 1);
-        if (who.x == who.y) return;  // one CTA had it all and wrote it
-        const int parts = who.y - who.x + 1;
-        for (int p = warp; p < parts; p += 4) {
+        write = who.x != who.y;  // else one CTA had it all and wrote it
+        const int parts = write ? who.y - who.x + 1 : 0;
+#pragma unroll 2
+        for (int p = sub; p < parts; p += kRowWarps) {
             const size_t slot = ((size_t)rt * nct + who.x + p) * 2 + (p == 0 ? 1 : 0);
             const float2 ml = a.part_ml[slot * tile_rows + n];
             const float *po = a.part + (slot * tile_rows + n) * D + lane * V;
+            float x[V];
+            if constexpr (V == 4)
+                *reinterpret_cast<float4 *>(x) = *reinterpret_cast<const float4 *>(po);
+            else
+                *reinterpret_cast<float2 *>(x) = *reinterpret_cast<const float2 *>(po);
             if (ml.x == -INFINITY) continue;
             const float mn = fmaxf(mt, ml.x);
             const float f0 = mt == -INFINITY ? 0.f : fast_exp2(mt - mn), f1 = fast_exp2(ml.x - mn);
             lt = lt * f0 + ml.y * f1;
 #pragma unroll
-            for (int v = 0; v < V; ++v) o[v] = o[v] * f0 + po[v] * f1;
+            for (int v = 0; v < V; ++v) o[v] = o[v] * f0 + x[v] * f1;
             mt = mn;
         }
+    }
+    if constexpr (kRowWarps > 1) {
         if (lane == 0) {
             sm_m[warp] = mt;
             sm_l[warp] = lt;
@@ -416,25 +430,24 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const CacheAttn a, int 
         for (int v = 0; v < V; ++v) sm_o[warp][lane * V + v] = o[v];
         __syncthreads();
         if (warp != 0) return;
-        float mm = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
+        mt = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
         lt = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) o[v] = 0.f;
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
             if (sm_m[w] == -INFINITY) continue;
-            const float f = fast_exp2(sm_m[w] - mm);
+            const float f = fast_exp2(sm_m[w] - mt);
             lt += sm_l[w] * f;
 #pragma unroll
             for (int v = 0; v < V; ++v) o[v] += sm_o[w][lane * V + v] * f;
         }
-        mt = mm;
     }
-    if (warp != 0) return;
+    if (!write) return;
     const float inv = lt > 0.f ? 1.f / lt : (lt == 0.f ? 0.f : lt);
     if (a.lse && lane == 0)
-        a.lse[orow] = dead ? 0.f : (lt == 0.f ? -INFINITY : (mt - E::kBias + log2f(lt)) * kLn2);
-    const size_t at = orow * D + lane * V;
+        a.lse[rr] = dead ? 0.f : (lt == 0.f ? -INFINITY : (mt - E::kBias + log2f(lt)) * kLn2);
+    const size_t at = (size_t)rr * D + lane * V;
     if (a.out_f32) {
 #pragma unroll
         for (int v = 0; v < V; ++v) static_cast<float *>(a.out)[at + v] = o[v] * inv;
@@ -468,9 +481,12 @@ cudaError_t launch_few(const CacheAttn &a, const CacheAttnPlan &p, cudaStream_t 
 template <typename E, int D>
 cudaError_t launch_join(const CacheAttn &a, const CacheAttnPlan &p, cudaStream_t st)
 {
+    const int rows = a.c.B * a.c.Hk * a.G * a.T;
+    // a row's parts, about: the CTAs of its row tile over the rows of work they share
+    const bool few = p.ctas / (a.c.B * a.c.Hk * a.Tp) <= 8;
     // programmatic launch: the join's CTAs start while the last units end and wait there
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(a.c.B * a.c.Hk * a.G * a.T);
+    cfg.gridDim = dim3(few ? (rows + 3) / 4 : rows);
     cfg.blockDim = dim3(128);
     cfg.stream = st;
     cudaLaunchAttribute at[1];
@@ -478,15 +494,14 @@ cudaError_t launch_join(const CacheAttn &a, const CacheAttnPlan &p, cudaStream_t
     at[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cache_join_kernel<E, D>, a, p.tile_rows, p.ctas);
+    return cudaLaunchKernelEx(&cfg, few ? cache_join_kernel<E, D, 1> : cache_join_kernel<E, D, 4>, a, p.tile_rows,
+                              p.ctas, rows);
 }
 
-// A stride of 0 over more than one element (an expanded tensor) has no tensor map.
 bool strides_map(const ab_cache &c)
 {
-    auto ok = [](int64_t s, int n) { return s != 0 || n == 1; };
-    return ok(c.k_row, c.page) && ok(c.k_head, c.Hk) && ok(c.k_page, c.n_pages) && ok(c.v_row, c.page) &&
-           ok(c.v_head, c.Hk) && ok(c.v_page, c.n_pages);
+    return stride_maps(c.k_row, c.page) && stride_maps(c.k_head, c.Hk) && stride_maps(c.k_page, c.n_pages) &&
+           stride_maps(c.v_row, c.page) && stride_maps(c.v_head, c.Hk) && stride_maps(c.v_page, c.n_pages);
 }
 
 }  // namespace

@@ -66,6 +66,11 @@ struct CacheMass {
     int *flag;
 };
 cudaError_t launch_cache_mass(const CacheMass &a, cudaStream_t st);
+// many query rows per key head, no plan (cache_mass_tiles.cu)
+cudaError_t launch_cache_mass_tiles(const CacheMass &a, cudaStream_t st);
+
+// A stride of 0 over more than one element (an expanded tensor) has no tensor map.
+inline bool stride_maps(int64_t stride, int n) { return stride != 0 || n == 1; }
 
 struct CacheKeep {
     ab_cache c;

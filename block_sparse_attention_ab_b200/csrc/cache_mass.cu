@@ -326,7 +326,11 @@ cudaError_t launch_d(const CacheMass &a, cudaStream_t st)
 
 cudaError_t launch_cache_mass(const CacheMass &a, cudaStream_t st)
 {
-    return a.c.dtype == AB_F16 ? launch_d<Fp16>(a, st) : launch_d<Bf16>(a, st);
+    const ab_cache &c = a.c;
+    if (!a.idx && a.G * a.T > 32 && stride_maps(c.k_row, c.page) && stride_maps(c.k_head, c.Hk) &&
+        stride_maps(c.k_page, c.n_pages))
+        return launch_cache_mass_tiles(a, st);
+    return c.dtype == AB_F16 ? launch_d<Fp16>(a, st) : launch_d<Bf16>(a, st);
 }
 
 }  // namespace ab

@@ -19,12 +19,13 @@
 #include "cache_common.cuh"
 #include "cache_kernels.h"
 #include "cache_sched.cuh"
-#include "tmap_host.h"
+#include "cache_tma.cuh"
 
 namespace ab {
 namespace {
 
 constexpr int kRows = 128;                 // query rows of a half: lanes of tensor memory
+static_assert(kUnit == kBoxRows, "a unit is one copy of a page of 64 tokens or more");
 constexpr int kEnt = 4;                    // page slots of a unit, at most (16-token pages)
 
 struct TileInfo {
@@ -74,22 +75,6 @@ struct TileSmem {
     static_assert(kAlloc <= 227 * 1024, "shared memory");
 };
 
-__device__ __forceinline__ void tma_load_4d(void *smem_dst, const void *tmap, uint64_t *bar, int x,
-                                            int y, int z, int w)
-{
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(smem_dst)),
-        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
-        : "memory");
-}
-
-template <typename E>
-constexpr uint32_t idesc(int M, int N, int a_mn, int b_mn)
-{
-    return sizeof(E) && E::kBias == 0.f ? idesc_bf16_f32(M, N, a_mn, b_mn) : idesc_f16_f32(M, N, a_mn, b_mn);
-}
-
 template <typename E, int D, int NH>
 __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
     cache_tile_kernel(const CacheAttn a, const __grid_constant__ CUtensorMap tmK,
@@ -111,6 +96,7 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
     const int cta = blockIdx.x, nct = gridDim.x, rt = blockIdx.y, row0 = rt * NH * kRows;
     const int page = a.c.page, shift = a.page_shift;
 
+    cudaTriggerProgrammaticLaunchCompletion();  // the join may come up and wait
     if (tid == 0) {
         for (int s = 0; s < L::kSlots; ++s) {
             mbar_init(&k_full[s], 1);   // and v_full behind it
@@ -553,23 +539,6 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
         tc_fence_after();
         tmem_dealloc(tmem, L::kTmemCols);
     }
-}
-
-// Map over the pages' (d, row, head, page); one box is 64 of d by the rows of a page (64 at
-// most), written with the 128-byte swizzle. A dimension of one element gets a stride that
-// is never used.
-bool page_map(CUtensorMap *tm, const ab_cache &c, const void *base, int64_t row, int64_t head, int64_t pg)
-{
-    EncodeTiledFn enc = tmap_encode_fn();
-    if (!enc) return false;
-    const cuuint64_t dims[4] = {(cuuint64_t)c.d, (cuuint64_t)c.page, (cuuint64_t)c.Hk, (cuuint64_t)c.n_pages};
-    const cuuint64_t strides[3] = {2 * (cuuint64_t)(row ? row : c.d), 2 * (cuuint64_t)(head ? head : c.d),
-                                   2 * (cuuint64_t)(pg ? pg : c.d)};
-    const cuuint32_t box[4] = {64, (cuuint32_t)(c.page < kUnit ? c.page : kUnit), 1, 1};
-    const cuuint32_t es[4] = {1, 1, 1, 1};
-    return enc(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <typename E, int D, int NH>

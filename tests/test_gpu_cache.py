@@ -400,6 +400,11 @@ def test_append_limits():
     ([517, 128], 1, 8, 128, 64, 40, FP),
     ([129, 255], 1, 12, 64, 128, 3, BF),
     ([2100, 64], 1, 2, 64, 16, 2, BF),
+    # more than 32 query rows, for some sequences only; more than one pass of 256
+    ([500, 90, 128], 2, 3, 128, 16, 60, BF),
+    ([1000, 3], 1, 12, 64, 32, 90, FP),
+    ([129, 700], 2, 5, 128, 128, 70, FP),
+    ([64, 0, 65], 3, 8, 64, 64, 33, BF),
 ])
 @pytest.mark.parametrize("use", ["all", "plan", "plan_per_token"])
 def test_mass_against_definition(lengths, Hk, G, d, page, T, dtype, use):
