@@ -41,6 +41,16 @@ ab_status check_cache(const ab_cache &c, bool pages = true)
     return AB_OK;
 }
 
+// pages that are written must not lie over one another (an expanded dimension)
+ab_status check_written(const ab_cache &c)
+{
+    using ab::stride_maps;
+    return stride_maps(c.k_row, c.page) && stride_maps(c.k_head, c.Hk) && stride_maps(c.k_page, c.n_pages) &&
+                   stride_maps(c.v_row, c.page) && stride_maps(c.v_head, c.Hk) && stride_maps(c.v_page, c.n_pages)
+               ? AB_OK
+               : AB_ERR_UNSUPPORTED;
+}
+
 ab_status check_tokens(const ab_tokens &t)
 {
     if (!t.p) return AB_ERR_NULL;
@@ -83,6 +93,7 @@ ab_status ab_cache_append(ab_cache c, ab_tokens k, ab_tokens v, int T, const int
 {
     NvtxRange nvtx("ab_cache_append");
     AB_TRY(check_cache(c));
+    AB_TRY(check_written(c));
     if (T <= 0) return AB_ERR_SHAPE;
     if (T > 1 << 20) return AB_ERR_RANGE;
     AB_TRY(check_tokens(k));
@@ -243,6 +254,7 @@ ab_status ab_cache_compact(ab_cache c, int budget, const int32_t *src, const int
 {
     NvtxRange nvtx("ab_cache_compact");
     AB_TRY(check_cache(c));
+    AB_TRY(check_written(c));
     if (!src || !n_keep) return AB_ERR_NULL;
     if (budget < 1 || budget > 1 << 30) return AB_ERR_RANGE;
     if (!aligned(src, 4) || !aligned(n_keep, 4)) return AB_ERR_ALIGN;

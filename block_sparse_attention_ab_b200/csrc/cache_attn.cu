@@ -511,6 +511,9 @@ CacheAttnPlan cache_attn_plan(const ab_cache &c, int G, int T, bool per_token)
     CacheAttnPlan p;
     const int rows = per_token ? G : G * T;
     int occ = 2;
+    // Over 8 x 16001..32760 slots of 8 heads, d = 128: 24 rows take 281 us in two tiles of 16
+    // rows here, which read K and V twice, and 188 us in the tile kernel; 16 rows take 159 us
+    // here and 206 us there.
     if (rows > 16 && strides_map(c)) {
         // up to three halves of 128 rows in one CTA (one CTA per SM), as evenly as they come
         const int halves = (rows + 127) / 128, tiles = (halves + 2) / 3;

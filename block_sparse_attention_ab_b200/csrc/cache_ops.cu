@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, kFar ? 1 : 2) cache_keep_kernel(cons
         for (int j = rank * kThreads + tid; j < m; j += cs * kThreads) src[j] = j;
         return;
     }
-    const int limit = a.recent > 0 ? a.next_pos[b] - a.recent : 0;
+    const int limit = a.recent > 0 ? (int)max((long long)a.next_pos[b] - a.recent, (long long)INT32_MIN) : 0;
     const int sl = (len + cs - 1) / cs, s0 = min(len, rank * sl), ns = min(len, s0 + sl) - s0;
     auto index_of = [&](int i) -> int64_t {  // of slot s0 + i in score and pos, or -1
         const int slot = s0 + i, pg = cache_page(a.c, b, slot >> page_shift, a.flag);

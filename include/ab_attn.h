@@ -435,7 +435,10 @@ ab_status ab_forward_host(const void *q_host, const void *k_host, const void *v_
  * and key head, mass is the attention weight received so far and pos the token's position.
  * The calls raise AB_FLAG_BAD_INDEX for a length outside 0 .. max_pages * page (clamped),
  * a token count outside 0 .. T (clamped) and a table entry outside 0 .. n_pages - 1 in a
- * place that has to be read or written (the page is skipped).
+ * place that has to be read or written (the page is skipped). Sequences may share pages that
+ * are only read (a common prefix); pages that a call writes (append, compact, and mass for the
+ * masses of every page) belong to one sequence, and their strides are not 0
+ * (AB_ERR_UNSUPPORTED).
  * ------------------------------------------------------------------------------------- */
 #define AB_MAX_TREE 128 /* new tokens per sequence of ab_cache_attn / _score / _mass */
 
@@ -473,7 +476,7 @@ typedef struct {
  * pos0   : int32 [B], or NULL for start.
  * Tokens that do not fit into max_pages * page slots are dropped (AB_FLAG_CACHE_FULL). A
  * start outside 0 .. max_pages * page raises AB_FLAG_BAD_INDEX and leaves the sequence as
- * it is. Different sequences must not share the pages that are written.
+ * it is.
  * Errors: AB_ERR_NULL, AB_ERR_SHAPE, AB_ERR_DTYPE, AB_ERR_UNSUPPORTED, AB_ERR_RANGE,
  * AB_ERR_ALIGN, AB_ERR_CUDA (the same for the calls below).
  */
@@ -516,7 +519,7 @@ ab_status ab_cache_score(ab_cache c, ab_tokens q, int Hq, int T, const int32_t *
  *             0 .. max_pages raises AB_FLAG_BAD_INDEX (skipped, clamped), a weight that is
  *             not finite and positive AB_FLAG_BAD_WEIGHT (its page is skipped).
  * out       : [B, Hq, T, d] contiguous, in the cache's type or AB_F32 (out_dtype); rows
- *             t >= n_tok[b] and rows that see nothing are 0.
+ *             t >= n_tok[b] and rows that see nothing are 0. Must not overlap an input.
  * lse       : optional fp32 [B, Hq, T]: ln of the denominator (0 for t >= n_tok[b], -inf
  *             for a row that sees nothing).
  * workspace : ab_cache_attn_workspace_size() bytes, contents need not be initialised. Calls
@@ -543,7 +546,8 @@ ab_status ab_cache_attn(ab_cache c, ab_tokens q, ab_tokens k, ab_tokens v, int H
  *            contiguous). sel: int32 [B, T] or NULL; a row outside 0 .. T - 1 raises
  *            AB_FLAG_BAD_INDEX and adds nothing.
  * idx, cnt, w, per_token : the plan of that call, or NULL; slots below length[b] - n outside
- *            the row's pages get nothing from it. Plan rows are indexed as q's rows are.
+ *            the row's pages get nothing from it. Plan rows are indexed as q's rows are and
+ *            ascend, as ab_select makes them.
  * mass_out : NULL for the cache's mass (in place), or [n_pages, Hk, page]; slots behind a
  *            sequence are not written. Needs mass.
  */

@@ -669,3 +669,146 @@ def test_long_cache_offsets_past_32_bits():
     ab.cache_mass(g, q.cuda(), lse)
     per_head = torch.stack([mass_[use, h].sum() for h in range(Hk)]).cpu()
     assert bool(((per_head - 4.0).abs() <= 1e-4).all())  # two tokens, two query heads each
+
+
+# ---------------------------------------------------------------- other calls, other places
+
+
+@pytest.mark.parametrize("T", [1, 30])
+def test_attn_and_mass_on_expanded_heads(T):
+    """One stored key head seen as three (stride 0): no tensor map, many rows or few."""
+    c = HostCache([333, 50], 1, 128, 64, BF, seed=51)
+    g = c.to_gpu()
+    q, k, v = c.randn(2, 6, T, 128), c.randn(2, 3, T, 128), c.randn(2, 3, T, 128)
+    wide = ab.KVCache(k=g.k.expand(-1, 3, -1, -1), v=g.v.expand(-1, 3, -1, -1), table=g.table, length=g.length,
+                      mass=torch.zeros(c.n_pages, 3, 64, device="cuda"))
+    c.Hk, c.k, c.v = 3, c.k.expand(-1, 3, -1, -1), c.v.expand(-1, 3, -1, -1)
+    c.mass = torch.zeros(c.n_pages, 3, 64)
+    out, lse = ab.cache_attn(wide, q.cuda(), k.cuda(), v.cuda(), want_lse=True)
+    _check_attn(out, lse, attn(c, q, k, v), BF)
+    ab.cache_mass(wide, q.cuda(), lse)
+    ref, tol = mass(c, q, lse.cpu())
+    assert bool(((wide.mass.cpu().to(F64) - ref).abs() <= tol + 1e-7).all())
+    for call in (lambda: ab.cache_append(wide, k.cuda(), v.cuda()),
+                 lambda: ab.cache_compact(wide, *ab.cache_keep(wide, 8))):
+        with pytest.raises(ab.AbError, match="UNSUPPORTED"):
+            call()
+
+
+def test_binding_refusals():
+    c = HostCache([40, 20], 2, 64, 16, BF, spare=4, seed=52)
+    g = c.to_gpu()
+    q, k = c.randn(2, 4, 3, 64).cuda(), c.randn(2, 2, 3, 64).cuda()
+    n = torch.ones(2, dtype=torch.int32, device="cuda")
+    with pytest.raises(TypeError, match="q must be"):
+        ab.cache_attn(g, q.half())
+    with pytest.raises(ValueError, match="k must be"):
+        ab.cache_attn(g, q, q, q)
+    with pytest.raises(ValueError, match="k and v go together"):
+        ab.cache_attn(g, q, k)
+    with pytest.raises(ValueError, match="same number of tokens"):
+        ab.cache_attn(g, q, k[:, :, :2], k[:, :, :2])
+    with pytest.raises(TypeError, match="n_tok must be"):
+        ab.cache_attn(g, q, n_tok=n.long())
+    with pytest.raises(ValueError, match="n_tok must be on"):
+        ab.cache_attn(g, q, n_tok=n.cpu())
+    with pytest.raises(ValueError, match="tree must be"):
+        ab.cache_attn(g, q, k, k, tree=torch.ones(2, 3, 4, dtype=torch.bool, device="cuda"))
+    with pytest.raises(ValueError, match="idx needs cnt"):
+        ab.cache_attn(g, q, idx=torch.zeros(2, 2, 1, c.max_pages, dtype=torch.int32, device="cuda"))
+    with pytest.raises(TypeError, match="out_dtype"):
+        ab.cache_attn(g, q, out_dtype=torch.float16)
+    with pytest.raises(ValueError, match="rows must be contiguous"):
+        ab.cache_append(g, k.transpose(2, 3).contiguous().transpose(2, 3), k)
+    with pytest.raises(ab.AbError, match="AB_ERR_SHAPE"):
+        ab.cache_score(g, torch.zeros(2, 3, 1, 64, dtype=BF, device="cuda"))
+    with pytest.raises(ab.AbError, match="AB_ERR_ALIGN"):
+        ab.cache_attn(g, torch.zeros(2, 4, 3, 72, dtype=BF, device="cuda")[..., 4:68])
+    with pytest.raises(ab.AbError, match="AB_ERR_WORKSPACE"):
+        ab.cache_attn(g, q, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ab.AbError, match="AB_ERR_UNSUPPORTED"):
+        ab.cache_append(g, k, k, start=g.length)
+    with pytest.raises(ValueError, match="mass"):
+        ab.cache_mass(ab.KVCache(k=g.k, v=g.v, table=g.table, length=g.length), q, torch.zeros(2, 4, 3, device="cuda"))
+    with pytest.raises(ValueError, match="mass must be"):
+        ab.KVCache(k=g.k, v=g.v, table=g.table, length=g.length, mass=g.mass[:, :1])
+    with pytest.raises(ValueError, match="one shape"):
+        ab.KVCache(k=g.k, v=g.v[:1], table=g.table, length=g.length)
+
+
+@pytest.mark.parametrize("T", [1, 24])
+def test_calls_on_two_streams_at_once(T):
+    """Calls in flight on two streams, each with its own workspace, give what they give alone."""
+    made = []
+    for seed in (61, 62):
+        c = HostCache([3000, 1999, 17], 2, 128, 64, BF, seed=seed)
+        made.append((c.to_gpu(), *(x.cuda() for x in (c.randn(3, 10, T, 128), c.randn(3, 2, T, 128),
+                                                      c.randn(3, 2, T, 128)))))
+    alone = [ab.cache_attn(g, q, k, v, want_lse=True) for g, q, k, v in made]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in made]
+    got = [[], []]
+    for _ in range(8):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(ab.cache_attn(*made[i], want_lse=True))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, l in got[i]:
+            assert torch.equal(o, alone[i][0]) and torch.equal(l, alone[i][1])
+
+
+def test_tree_step_captured_and_replayed():
+    """A drafted tree's step (the tile kernels) in a graph, replayed on changing inputs."""
+    B, Hk, G, d, page, T = 2, 2, 4, 64, 64, 16
+
+    def fresh():
+        c = HostCache([300, 65], Hk, d, page, FP, spare=12, max_pages=9, seed=71)
+        for b in range(B):
+            c.allocate(b, 570)
+        return c, c.to_gpu()
+    c, a = fresh()
+    _, e = fresh()
+    toks = [[c.randn(B, h, T, d).cuda() for h in (Hk * G, Hk, Hk)] + [_tree(B, T, c.g).cuda()] for _ in range(3)]
+    q, k, v, tree = (torch.zeros_like(t) for t in toks[0])
+
+    def step(cache, q, k, v, tree):
+        out, lse = ab.cache_attn(cache, q, k, v, tree=tree, want_lse=True)
+        ab.cache_append(cache, k, v)
+        ab.cache_mass(cache, q, lse)
+        return out
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step(fresh()[1], q, k, v, tree)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out = step(a, q, k, v, tree)
+    torch.cuda.synchronize()
+    for t in toks:
+        for dst, x in zip((q, k, v, tree), t):
+            dst.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, step(e, *t))
+    for x in ("k", "v", "ksum", "mass", "length"):
+        assert torch.equal(getattr(a, x), getattr(e, x)), x
+
+
+def test_one_token_of_a_full_table_and_of_many_sequences():
+    """Every slot of the table in use; 300 sequences of a few tokens, some empty."""
+    c = HostCache([64, 63], 1, 64, 16, BF, max_pages=4, seed=81)
+    q, k, v = c.randn(2, 2, 1, 64), c.randn(2, 1, 1, 64), c.randn(2, 1, 1, 64)
+    out, lse = ab.cache_attn(c.to_gpu(), q.cuda(), k.cuda(), v.cuda(), want_lse=True)
+    _check_attn(out, lse, attn(c, q, k, v), BF)
+    many = HostCache([(7 * b) % 40 for b in range(300)], 1, 64, 16, FP, seed=82)
+    q, k, v = many.randn(300, 3, 1, 64), many.randn(300, 1, 1, 64), many.randn(300, 1, 1, 64)
+    g = many.to_gpu()
+    out, lse = ab.cache_attn(g, q.cuda(), k.cuda(), v.cuda(), want_lse=True)
+    _check_attn(out, lse, attn(many, q, k, v), FP)
+    flag = _flag()
+    sc = ab.cache_score(g, q.cuda(), dev_flag=flag)
+    ref, rel = score(many, q)
+    assert ab.check_flag(flag) == 0
+    assert bool(((sc.cpu().to(F64) - ref).abs() <= rel * ref + 1e-30).all())
