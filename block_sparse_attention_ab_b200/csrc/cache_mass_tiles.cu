@@ -3,8 +3,8 @@
 //
 // S^T = K Q^T with 128 keys as the rows of the product and up to 256 query rows as its
 // columns, so a thread owns a key and adds its weights over the query rows in registers: no
-// exchange between threads. One CTA per SM: a warp copies key tiles (TMA through the page map,
-// the sequence's last tile by its own lanes with zeros where no key is), a warp issues the
+// exchange between threads. One CTA per SM: a warp copies key tiles (TMA through the page map;
+// what lies in rows that are no key's goes to sums that nobody writes), a warp issues the
 // products into two tensor memory buffers of 256 columns, and two sets of four warps take the
 // buffers in turn: p = 2^(s scale - lse), summed in fp32. Bound by the exponentials once there
 // are more than about 160 rows (16 a cycle and SM), by reading K below that; a warp-level
@@ -168,7 +168,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool ok = true;
         while (ok && next_piece(pc, nullptr)) {
             const int slots = (pc.len + page - 1) >> shift, rows = pc.n * a.G;
-            const char *base = static_cast<const char *>(a.c.k) + 2 * pc.hk * a.c.k_head;
             for (int r0 = 0; ok && r0 < rows; r0 += kRows) {
                 const int batch = 32 / nent;  // units whose pages are looked up together
                 int pages = -1, behind = batch;
@@ -179,43 +178,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pages = uu < pc.u1 && slot < slots ? cache_page(a.c, pc.b, slot, a.flag) : -1;
                     }
                     const int pg = __shfl_sync(~0u, pages, (behind * nent + lane) & 31);
-                    const bool whole = __all_sync(~0u, lane >= nent || pg >= 0) && (u + 1) * kKeys <= pc.len;
                     if (it >= NS) ok = wait(&k_empty[s], par_e);
                     if (!ok) break;
                     if (lane < nent) info[it % kInfos].page[lane] = pg;
                     __syncwarp();  // the info is written before the barrier is armed
                     uint8_t *tile = smem + L::kRing + s * L::kTile;
-                    if (whole) {
-                        if (lane == 0) mbar_arrive_expect_tx(&k_full[s], L::kTile);
-                        __syncwarp();
-                        loaded |= 1u << s;
-                        // lane: a box of rows; pages above 64 tokens take two
-                        const int from = page > kBoxRows ? 0 : lane;
-                        const int bp = __shfl_sync(~0u, pg, from & 31);
-                        if (lane < boxes) {
-                            const int row = page > kBoxRows ? lane * kBoxRows : 0;
+                    // lane: a box of rows; pages above 64 tokens take two
+                    const int bp = __shfl_sync(~0u, pg, page > kBoxRows ? 0 : lane);
+                    const bool has = lane < boxes && bp >= 0;
+                    const uint32_t bytes = __popc(__ballot_sync(~0u, has)) * box_rows * (D * 2);
+                    if (lane == 0) {
+                        if (bytes)
+                            mbar_arrive_expect_tx(&k_full[s], bytes);
+                        else
+                            mbar_arrive(&k_full[s]);
+                    }
+                    __syncwarp();
+                    loaded = bytes ? loaded | 1u << s : loaded & ~(1u << s);
+                    if (has) {
+                        const int row = page > kBoxRows ? lane * kBoxRows : 0;
 #pragma unroll
-                            for (int y = 0; y < D / 64; ++y)
-                                tma_load_4d(tile + y * L::kTileBox + lane * box_rows * 128, &tmK, &k_full[s], y * 64,
-                                            row, pc.hk, bp);
-                        }
-                    } else {
-                        loaded &= ~(1u << s);
-                        constexpr int kChunks = D / 8;
-#pragma unroll 8
-                        for (int i = lane; i < kKeys * kChunks; i += 32) {
-                            const int j = i / kChunks, c = i % kChunks;
-                            const int p = __shfl_sync(~0u, pg, page >= kKeys ? 0 : j >> shift);
-                            const int64_t r = j & (page - 1);
-                            uint4 x = make_uint4(0, 0, 0, 0);
-                            if (p >= 0 && u * kKeys + j < pc.len)
-                                x = ldg_stream(base + 2 * (p * a.c.k_page + r * a.c.k_row) + c * 16);
-                            *reinterpret_cast<uint4 *>(tile + (c >> 3) * L::kTileBox + j * 128 +
-                                                       (((c & 7) ^ (j & 7)) << 4)) = x;
-                        }
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&k_full[s]);
+                        for (int y = 0; y < D / 64; ++y)
+                            tma_load_4d(tile + y * L::kTileBox + lane * box_rows * 128, &tmK, &k_full[s], y * 64, row,
+                                        pc.hk, bp);
                     }
                     phase ^= 1u << s;
                     __syncwarp();

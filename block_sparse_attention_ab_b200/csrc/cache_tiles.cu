@@ -12,8 +12,10 @@
 // Units whose 64 keys all exist come by TMA through a map over (d, row, head, page): the page's
 // number is a coordinate, so any strides and page sizes do, and pages of 16 and 32 tokens are 4
 // and 2 boxes of one tile. The others (a sequence's last keys, the new tokens, a tile with an
-// absent page) are written by the copying warps' own lanes, with zeros where no key is, in the
-// same swizzle.
+// absent page) come the same way, the new tokens through a map of their own; a key that does
+// not exist is masked out of S whatever its row holds, and its row of V is set to zero once the
+// copy is there (0 * NaN is NaN). New tokens with a stride of 0 are written by the copying
+// warps' lanes.
 #include <cstdint>
 
 #include "cache_common.cuh"
@@ -64,10 +66,10 @@ struct TileSmem {
     static constexpr int kInfo = kKv + kSlots * kTile;
     static constexpr int kBars = (kInfo + kInfos * (int)sizeof(TileInfo) + 7) / 8 * 8;
     // k_full, v_full, k_empty, v_empty [kSlots], s_free [kSBufs], s_full [NH][4], p_full,
-    // q_full, pv_done [NH], drain [2]. A parity wait is exact for a waiter that sees every phase:
+    // q_full, pv_done [NH], drain [2], edge. A parity wait is exact for a waiter that sees every phase:
     // s_full (its units in turn) and pv_done belong to a half, the others to one of the
     // four warps, which waits for every use in turn.
-    static constexpr int kNumBars = 2 * kSlots + kSBufs + 7 * NH + 2;
+    static constexpr int kNumBars = 2 * kSlots + kSBufs + 7 * NH + 3;
     static constexpr int kMisc = kBars + kNumBars * 8;  // tensor memory address, abort flag
     static constexpr int kRun = kMisc + 16;
     static constexpr int kBytes = kRun + (int)sizeof(RunSmem);
@@ -78,7 +80,8 @@ struct TileSmem {
 template <typename E, int D, int NH>
 __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
     cache_tile_kernel(const CacheAttn a, const __grid_constant__ CUtensorMap tmK,
-                      const __grid_constant__ CUtensorMap tmV)
+                      const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKn,
+                      const __grid_constant__ CUtensorMap tmVn, bool fresh_map)
 {
     using L = TileSmem<D, NH>;
     constexpr int NK = L::kK, NV = L::kV, NI = L::kInfos, SB = L::kSBufs;
@@ -88,7 +91,7 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
     uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + L::kBars), *v_full = k_full + NK;
     uint64_t *k_empty = v_full + NV, *v_empty = k_empty + NK, *s_free = v_empty + NV, *s_full = s_free + SB;
     uint64_t *p_full = s_full + 4 * NH, *q_full = p_full + NH, *pv_done = q_full + NH;
-    uint64_t *drain = pv_done + NH;
+    uint64_t *drain = pv_done + NH, *edge_bar = drain + 2;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMisc);
     volatile int *abort = reinterpret_cast<volatile int *>(smem + L::kMisc + 8);
     RunSmem &run_sm = *reinterpret_cast<RunSmem *>(smem + L::kRun);
@@ -111,6 +114,7 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
         }
         mbar_init(&drain[0], 1);
         mbar_init(&drain[1], 1);
+        mbar_init(edge_bar, 1);
         *abort = 0;
         fence_barrier_init();
     }
@@ -131,7 +135,7 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
     };
     if (warp == L::kWarpK || warp == L::kWarpV) {
         const bool is_k = warp == L::kWarpK;
-        const CUtensorMap *tm = is_k ? &tmK : &tmV;
+        const CUtensorMap *tm = is_k ? &tmK : &tmV, *tmn = is_k ? &tmKn : &tmVn;
         uint64_t *full = is_k ? k_full : v_full, *empty = is_k ? k_empty : v_empty;
         uint8_t *ring = smem + (is_k ? L::kKv : L::kVAt);
         const int ns = is_k ? NK : NV;
@@ -144,6 +148,7 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
         int it = 0, s = 0;                  // units so far, their ring slot
         uint32_t par_e = 1;                 // parity of the slots' last release
         uint32_t phase = 0, loaded = 0;     // bit s: parity of slot s's next tile; its last one was copied
+        uint32_t edges = 0;                 // V copies that were waited for here
         bool ok = true;
         while (ok && next_piece(a, run, nct, pc, nullptr)) {
             if (row0 >= group_rows(a, pc.g)) continue;
@@ -175,40 +180,66 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
                     if (lane == 0) ti.partial = !whole;
                 }
                 uint8_t *tile = ring + s * L::kTile;
-                if (whole) {
+                const int j0 = (u - pc.g.ctx_units) * kUnit;  // first new token of the unit
+                // rows of V that are no key's have to be zero
+                const bool mend = !is_k && (ctx ? !whole : j0 + kUnit > pc.g.n && pc.g.n < a.T);
+                loaded &= ~(1u << s);
+                if (ctx || fresh_map) {
+                    const unsigned has = ctx ? __ballot_sync(~0u, lane < nent && e.page >= 0) : 1u;
+                    const uint32_t bytes = ctx ? __popc(has) * box_rows * (D * 2) : L::kTile;
+                    uint64_t *bar = mend ? edge_bar : &full[s];
                     __syncwarp();  // the info is written before the barrier is armed
-                    if (lane == 0) mbar_arrive_expect_tx(&full[s], L::kTile);
+                    if (lane == 0) {
+                        if (bytes)
+                            mbar_arrive_expect_tx(bar, bytes);
+                        else if (!mend)
+                            mbar_arrive(bar);
+                    }
                     __syncwarp();
-                    loaded |= 1u << s;
-                    if (lane < nent) {
+                    if (bytes && !mend) loaded |= 1u << s;
+                    if (has >> lane & 1) {
 #pragma unroll
-                        for (int y = 0; y < L::kBoxes; ++y)
-                            tma_load_4d(tile + lane * box_rows * 128 + y * (kUnit * 128), tm, &full[s], y * 64, r0,
-                                        pc.hk, e.page);
+                        for (int y = 0; y < L::kBoxes; ++y) {
+                            uint8_t *d = tile + lane * box_rows * 128 + y * (kUnit * 128);
+                            if (ctx)
+                                tma_load_4d(d, tm, bar, y * 64, r0, pc.hk, e.page);
+                            else
+                                tma_load_4d(d, tmn, bar, y * 64, j0, pc.hk, pc.g.b);
+                        }
+                    }
+                    __syncwarp();
+                    if (mend) {
+                        if (bytes) {
+                            ok = wait(edge_bar, edges);
+                            if (!ok) {
+                                drain_wait(edge_bar, edges & 1);
+                                break;
+                            }
+                            ++edges;
+                        }
+                        for (int j = 0; j < kUnit; ++j) {
+                            const int en = page >= kUnit ? 0 : j >> shift, r = (u * kUnit + j) & (page - 1);
+                            const int pg = __shfl_sync(~0u, e.page, en), valid = __shfl_sync(~0u, e.valid, en);
+                            if (ctx ? pg >= 0 && r < valid : j0 + j < pc.g.n) continue;
+                            if (lane < L::kBoxes * 8)
+                                *reinterpret_cast<uint4 *>(tile + (lane >> 3) * (kUnit * 128) + j * 128 +
+                                                           (lane & 7) * 16) = make_uint4(0, 0, 0, 0);
+                        }
                     }
                 } else {
-                    loaded &= ~(1u << s);
                     constexpr int kChunks = D / 8;
                     const ab_tokens &nt = is_k ? a.k : a.v;
-                    const char *fresh_rows = static_cast<const char *>(nt.p) + 2 * (pc.g.b * nt.sb + pc.hk * nt.sh);
-                    const char *base = static_cast<const char *>(is_k ? a.c.k : a.c.v) +
-                                       2 * pc.hk * (is_k ? a.c.k_head : a.c.v_head);
-                    const int64_t spage = is_k ? a.c.k_page : a.c.v_page, srow = is_k ? a.c.k_row : a.c.v_row;
-                    const int j0 = (u - pc.g.ctx_units) * kUnit;
+                    const char *rows = static_cast<const char *>(nt.p) + 2 * (pc.g.b * nt.sb + pc.hk * nt.sh);
 #pragma unroll 8
                     for (int i = lane; i < kUnit * kChunks; i += 32) {
-                        const int j = i / kChunks, c = i % kChunks, en = page >= kUnit ? 0 : j >> shift;
-                        const int pg = __shfl_sync(~0u, e.page, en), valid = __shfl_sync(~0u, e.valid, en);
+                        const int j = i / kChunks, c = i % kChunks;
                         uint4 x = make_uint4(0, 0, 0, 0);
-                        if (!ctx) {
-                            if (j0 + j < pc.g.n) x = ldg_stream(fresh_rows + 2 * (j0 + j) * nt.st + c * 16);
-                        } else {
-                            const int r = (u * kUnit + j) & (page - 1);
-                            if (pg >= 0 && r < valid) x = ldg_stream(base + 2 * (pg * spage + r * srow) + c * 16);
-                        }
+                        if (j0 + j < pc.g.n) x = ldg_stream(rows + 2 * (j0 + j) * nt.st + c * 16);
                         *reinterpret_cast<uint4 *>(tile + (c >> 3) * (kUnit * 128) + j * 128 +
                                                    (((c & 7) ^ (j & 7)) << 4)) = x;
                     }
+                }
+                if (mend || !(ctx || fresh_map)) {
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&full[s]);
@@ -384,11 +415,16 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
                         const uint8_t *tr = a.tree + ((size_t)b * a.T + t) * a.T + j0;
                         int j = 0;
                         if ((reinterpret_cast<uintptr_t>(tr) & 3) == 0) {  // four bytes at a time
-#pragma unroll 4
-                            for (; j + 4 <= nv; j += 4) {
-                                const uint32_t x = __vcmpne4(*reinterpret_cast<const uint32_t *>(tr + j), 0);
-                                sees |= (uint64_t)((x & 1) | (x >> 7 & 2) | (x >> 14 & 4) | (x >> 21 & 8)) << j;
+                            uint32_t w[kUnit / 4];
+#pragma unroll
+                            for (int i = 0; i < kUnit / 4; ++i)
+                                w[i] = 4 * i + 4 <= nv ? *reinterpret_cast<const uint32_t *>(tr + 4 * i) : 0;
+#pragma unroll
+                            for (int i = 0; i < kUnit / 4; ++i) {
+                                const uint32_t x = __vcmpne4(w[i], 0);
+                                sees |= (uint64_t)((x & 1) | (x >> 7 & 2) | (x >> 14 & 4) | (x >> 21 & 8)) << (4 * i);
                             }
+                            j = nv & ~3;
                         }
 #pragma unroll 4
                         for (; j < nv; ++j) sees |= (uint64_t)(tr[j] != 0) << j;
@@ -541,25 +577,29 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
     }
 }
 
+struct Maps {
+    CUtensorMap k, v, kn, vn;
+    bool fresh;  // kn and vn are there
+};
+
 template <typename E, int D, int NH>
-cudaError_t launch_one(const CacheAttn &a, int nct, const CUtensorMap &tk, const CUtensorMap &tv, cudaStream_t st)
+cudaError_t launch_one(const CacheAttn &a, int nct, const Maps &m, cudaStream_t st)
 {
     using L = TileSmem<D, NH>;
     auto kern = cache_tile_kernel<E, D, NH>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
     if (e != cudaSuccess) return e;
-    kern<<<dim3(nct, a.row_tiles), L::kThreads, L::kAlloc, st>>>(a, tk, tv);
+    kern<<<dim3(nct, a.row_tiles), L::kThreads, L::kAlloc, st>>>(a, m.k, m.v, m.kn, m.vn, m.fresh);
     return cudaGetLastError();
 }
 
 template <typename E, int D>
-cudaError_t launch_halves(const CacheAttn &a, const CacheAttnPlan &p, const CUtensorMap &tk, const CUtensorMap &tv,
-                          cudaStream_t st)
+cudaError_t launch_halves(const CacheAttn &a, const CacheAttnPlan &p, const Maps &m, cudaStream_t st)
 {
     switch (p.tile_rows / kRows) {
-    case 1: return launch_one<E, D, 1>(a, p.ctas, tk, tv, st);
-    case 2: return launch_one<E, D, 2>(a, p.ctas, tk, tv, st);
-    default: return launch_one<E, D, 3>(a, p.ctas, tk, tv, st);
+    case 1: return launch_one<E, D, 1>(a, p.ctas, m, st);
+    case 2: return launch_one<E, D, 2>(a, p.ctas, m, st);
+    default: return launch_one<E, D, 3>(a, p.ctas, m, st);
     }
 }
 
@@ -567,13 +607,15 @@ cudaError_t launch_halves(const CacheAttn &a, const CacheAttnPlan &p, const CUte
 
 cudaError_t launch_cache_tiles(const CacheAttn &a, const CacheAttnPlan &p, cudaStream_t st)
 {
-    CUtensorMap tk, tv;
+    Maps m;
     const ab_cache &c = a.c;
-    if (!page_map(&tk, c, c.k, c.k_row, c.k_head, c.k_page) || !page_map(&tv, c, c.v, c.v_row, c.v_head, c.v_page))
+    if (!page_map(&m.k, c, c.k, c.k_row, c.k_head, c.k_page) || !page_map(&m.v, c, c.v, c.v_row, c.v_head, c.v_page))
         return cudaErrorInvalidValue;
-    if (c.dtype == AB_F16)
-        return c.d == 64 ? launch_halves<Fp16, 64>(a, p, tk, tv, st) : launch_halves<Fp16, 128>(a, p, tk, tv, st);
-    return c.d == 64 ? launch_halves<Bf16, 64>(a, p, tk, tv, st) : launch_halves<Bf16, 128>(a, p, tk, tv, st);
+    m.kn = m.k;
+    m.vn = m.v;
+    m.fresh = a.k.p && token_map(&m.kn, c, a.k, a.T) && token_map(&m.vn, c, a.v, a.T);
+    if (c.dtype == AB_F16) return c.d == 64 ? launch_halves<Fp16, 64>(a, p, m, st) : launch_halves<Fp16, 128>(a, p, m, st);
+    return c.d == 64 ? launch_halves<Bf16, 64>(a, p, m, st) : launch_halves<Bf16, 128>(a, p, m, st);
 }
 
 }  // namespace ab

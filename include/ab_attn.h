@@ -525,8 +525,8 @@ ab_status ab_cache_score(ab_cache c, ab_tokens q, int Hq, int T, const int32_t *
  * workspace : ab_cache_attn_workspace_size() bytes, contents need not be initialised. Calls
  *             that may run at the same time need one each.
  * The new tokens' own keys and values are read from k, v, not from the cache: append the
- * accepted ones afterwards. Values in slots and rows that a sequence cannot see are never
- * read; a value that some row of a (sequence, key head) sees takes part in that sequence's
+ * accepted ones afterwards. Whatever lies in slots and rows that a sequence cannot see, a NaN
+ * too, takes no part; a value that some row of a (sequence, key head) sees takes part in that sequence's
  * products, so a NaN or an infinity in a drafted token's value reaches its siblings.
  * Every sum runs in an order that the lengths and counts fix: equal calls give equal bits.
  */
