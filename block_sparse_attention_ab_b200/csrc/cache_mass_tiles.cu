@@ -5,8 +5,9 @@
 // columns, so a thread owns a key and adds its weights over the query rows in registers: no
 // exchange between threads. One CTA per SM: a warp copies key tiles (TMA through the page map;
 // what lies in rows that are no key's goes to sums that nobody writes), a warp issues the
-// products into two tensor memory buffers of 256 columns, and two sets of four warps take the
-// buffers in turn: p = 2^(s scale - lse), summed in fp32. Bound by the exponentials once there
+// products into two tensor memory buffers of 256 columns, and eight warps per buffer (each
+// thread every other 32 of its key's columns; the two sums meet in shared memory) compute
+// p = 2^(s scale - lse), summed in fp32. Bound by the exponentials once there
 // are more than about 160 rows (16 a cycle and SM), by reading K below that; a warp-level
 // product with shared query fragments (cache_mass.cu) took 361 us against {MASS_US} us for 192
 // rows over 2 x 60000..118800 slots of 8 heads.
@@ -19,8 +20,9 @@
 namespace ab {
 namespace {
 
-constexpr int kThreads = 320;  // two sets of four warps, copy warp, product warp
-constexpr int kWarpK = 8, kWarpS = 9;
+constexpr int kSums = 512;     // threads that add: two buffers, two halves of the columns, four warps
+constexpr int kThreads = kSums + 64;
+constexpr int kWarpK = 16, kWarpS = 17;
 constexpr int kKeys = 128;     // keys per unit
 constexpr int kRows = 256;     // query rows per pass
 constexpr int kEnt = 8;        // page slots of a unit, at most (16-token pages)
@@ -39,12 +41,13 @@ struct MassSmem {
     static constexpr int kRing = kQ;
     static constexpr int kLse = kRing + kSlots * kTile;  // -log-sum in base 2 [kRows]
     static constexpr int kBound = kLse + kRows * 4;      // the row sees slots below this
-    static constexpr int kInfo = kBound + kRows * 4;
+    static constexpr int kPart = kBound + kRows * 4;     // the second half's sums [2][2][kKeys]
+    static constexpr int kInfo = kPart + 4 * kKeys * 4;
     static constexpr int kBars = kInfo + kInfos * (int)sizeof(TileInfo);
     // k_full, k_empty [kSlots], s_full, s_free [2], q_full, drain
     static constexpr int kNumBars = 2 * kSlots + 6;
     static constexpr int kMisc = kBars + kNumBars * 8;  // tensor memory address, abort flag, run
-    static constexpr int kBytes = kMisc + 16 + 16 * 8 + 16;
+    static constexpr int kBytes = kMisc + 16 + 18 * 8 + 16;
     static constexpr int kAlloc = kBytes + 1024;
     // info slot i is rewritten for unit i + kInfos, whose tile waits for the product of unit i +
     // kInfos - kSlots, which waits until the sets have read buffers (and info) of two units before
@@ -61,13 +64,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = align_smem_1024(smem_raw);
     float *nlse = reinterpret_cast<float *>(smem + L::kLse);
     int *bound = reinterpret_cast<int *>(smem + L::kBound);
+    float *part = reinterpret_cast<float *>(smem + L::kPart);
     TileInfo *info = reinterpret_cast<TileInfo *>(smem + L::kInfo);
     uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + L::kBars), *k_empty = k_full + NS;
     uint64_t *s_full = k_empty + NS, *s_free = s_full + 2, *q_full = s_free + 2, *drain = q_full + 1;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::kMisc);
     volatile int *abort = reinterpret_cast<volatile int *>(smem + L::kMisc + 8);
     long long *scan = reinterpret_cast<long long *>(smem + L::kMisc + 16);
-    int *found = reinterpret_cast<int *>(smem + L::kMisc + 16 + 16 * 8);
+    int *found = reinterpret_cast<int *>(smem + L::kMisc + 16 + 18 * 8);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int page = a.c.page, shift = a.page_shift;
 
@@ -78,9 +82,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(&s_full[s], 1);
-            mbar_init(&s_free[s], 4);
+            mbar_init(&s_free[s], 8);
         }
-        mbar_init(q_full, 256);
+        mbar_init(q_full, kSums);
         mbar_init(drain, 1);
         *abort = 0;
         fence_barrier_init();
@@ -254,9 +258,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
         }
     } else {
-        // ---- two sets of four warps. After a failed wait they run out their loops (they meet
-        // at named barriers) and write nothing.
-        const int set = warp >> 2, th = tid & 127;
+        // ---- the sums. After a failed wait these warps run out their loops (they meet at named
+        // barriers) and write nothing.
+        const int set = warp >> 2 & 1, half = warp >> 3, th = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         bool ok = true;
         int it = 0;
@@ -264,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int rows = pc.n * a.G, old_len = pc.len - pc.n;
             if (rows == 0) {  // nothing to add: the masses as they are
                 if (a.out != a.c.mass)
-                    for (int key = pc.u0 * kKeys + tid; key < min(pc.len, pc.u1 * kKeys); key += 256) {
+                    for (int key = pc.u0 * kKeys + tid; key < min(pc.len, pc.u1 * kKeys); key += kSums) {
                         const int pg = cache_page(a.c, pc.b, key >> shift, a.flag);
                         if (pg < 0) continue;
                         const int64_t at = ((int64_t)pg * a.c.Hk + pc.hk) * page + (key & (page - 1));
@@ -274,14 +278,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             for (int r0 = 0; r0 < rows; r0 += kRows) {
                 const int nr = min(kRows, rows - r0), np = (nr + 31) & ~31;
-                // the products that read the last rows are done when both sets are here
-                asm volatile("bar.sync 1, 256;" ::: "memory");
+                // the products that read the last rows are done when everybody is here
+                asm volatile("bar.sync 1, %0;" ::"n"(kSums) : "memory");
                 auto row_of = [&](int r) -> int {  // row of q and lse, or -1
                     if (r >= rows) return -1;
                     const int k = r / a.G, t = a.sel ? a.sel[(size_t)pc.b * a.T + k] : k;
                     return (unsigned)t < (unsigned)a.T ? t : -1;
                 };
-                for (int i = tid; i < np; i += 256) {
+                for (int i = tid; i < np; i += kSums) {
                     const int r = r0 + i, t = row_of(r);
                     float nl = -INFINITY;
                     if (t >= 0) {
@@ -296,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 constexpr int kChunks = D / 8;
 #pragma unroll 4
-                for (int i = tid; i < np * kChunks; i += 256) {
+                for (int i = tid; i < np * kChunks; i += kSums) {
                     const int r = i / kChunks, c = i % kChunks, t = row_of(r0 + r);
                     uint4 x = make_uint4(0, 0, 0, 0);
                     if (t >= 0) {
@@ -308,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 fence_proxy_async_smem();
                 mbar_arrive(q_full);
-                asm volatile("bar.sync 1, 256;" ::: "memory");
+                asm volatile("bar.sync 1, %0;" ::"n"(kSums) : "memory");
                 for (int u = pc.u0; u < pc.u1; ++u, ++it) {
                     if ((it & 1) != set) continue;
                     if (ok) ok = wait(&s_full[set], it >> 1);
@@ -316,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int key = u * kKeys + th;
                     int64_t at = -1;
                     float sum[4] = {0.f, 0.f, 0.f, 0.f}, old = 0.f;
-                    if (ok && key < pc.len) {
+                    if (half == 0 && ok && key < pc.len) {
                         const int pg = info[it % kInfos].page[page >= kKeys ? 0 : th >> shift];
                         if (pg >= 0) {
                             at = ((int64_t)pg * a.c.Hk + pc.hk) * page + (key & (page - 1));
@@ -325,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     __syncwarp();
                     const bool edge = (u + 1) * kKeys > old_len;
-                    for (int c0 = 0; c0 < np; c0 += 32) {
+                    for (int c0 = 32 * half; c0 < np; c0 += 64) {
                         uint32_t x[32];
                         tmem_ld32(tmem + lanes + set * kRows + c0, x);
                         tmem_wait_ld();
@@ -350,7 +354,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&s_free[set]);
-                    if (at >= 0) a.out[at] = old + ((sum[0] + sum[1]) + (sum[2] + sum[3]));
+                    // the halves meet; a buffer's next sums go to the other place
+                    const float mine = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    float *other = part + (2 * set + (it >> 1 & 1)) * kKeys + th;
+                    if (half == 1) *other = mine;
+                    asm volatile("bar.sync %0, 256;" ::"r"(2 + set) : "memory");
+                    if (at >= 0) a.out[at] = old + (mine + *other);
                 }
             }
         }
