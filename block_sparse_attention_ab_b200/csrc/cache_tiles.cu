@@ -77,7 +77,10 @@ struct TileSmem {
     static_assert(kAlloc <= 227 * 1024, "shared memory");
 };
 
-template <typename E, int D, int NH>
+// kSplit (NH = 2): the two halves are the same 128 rows, and take every other unit; each has its
+// own running maximum, sum and accumulator, which meet at a piece's end. One half's chain from S
+// to P is then hidden behind the other's (24 rows per key head: {SPLIT_US}).
+template <typename E, int D, int NH, bool kSplit>
 __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
     cache_tile_kernel(const CacheAttn a, const __grid_constant__ CUtensorMap tmK,
                       const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmKn,
@@ -96,7 +99,9 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
     volatile int *abort = reinterpret_cast<volatile int *>(smem + L::kMisc + 8);
     RunSmem &run_sm = *reinterpret_cast<RunSmem *>(smem + L::kRun);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int cta = blockIdx.x, nct = gridDim.x, rt = blockIdx.y, row0 = rt * NH * kRows;
+    const int cta = blockIdx.x, nct = gridDim.x, rt = blockIdx.y;
+    constexpr int kTileRows = kSplit ? kRows : NH * kRows;
+    const int row0 = rt * kTileRows;
     const int page = a.c.page, shift = a.page_shift;
 
     cudaTriggerProgrammaticLaunchCompletion();  // the join may come up and wait
@@ -109,7 +114,7 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
         for (int h = 0; h < NH; ++h) {
             for (int i = 0; i < 4; ++i) mbar_init(&s_full[4 * h + i], 1);
             mbar_init(&p_full[h], 4);
-            mbar_init(&q_full[h], 128);
+            mbar_init(&q_full[h], kSplit ? 256 : 128);
             mbar_init(&pv_done[h], 1);
         }
         mbar_init(&drain[0], 1);
@@ -260,7 +265,7 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
         constexpr uint32_t idesc_s = idesc<E>(kRows, kUnit, 0, 0);
         const uint64_t qd = smem_desc_sw128(smem_u32(smem), 16, 1024);
         const uint64_t kd0 = smem_desc_sw128(smem_u32(smem + L::kKv), 16, 1024);
-        int s = 0;                        // ring slot of the next unit
+        int s = 0, it = 0;                // ring slot of the next unit, units so far
         int buf = 0;                      // S buffer of the next job
         uint32_t tiles = 0;               // bit s: parity of slot s's next tile
         uint32_t turn = 0, phase_q = 0;   // two bits per half: its next S's barrier; bit h: its next Q
@@ -269,27 +274,29 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
         while (ok && next_piece(a, run, nct, pc, nullptr)) {
             const int rows = group_rows(a, pc.g) - row0;
             if (rows <= 0) continue;
-            const int na = min(NH, (rows + kRows - 1) / kRows);  // halves with rows in this piece
+            // halves with rows in this piece (kSplit: one Q)
+            const int na = kSplit ? 1 : min(NH, (rows + kRows - 1) / kRows);
             for (int h = 0; ok && h < na; ++h) {
                 ok = wait(&q_full[h], phase_q >> h);
                 phase_q ^= 1u << h;
             }
-            for (int n = pc.u1 - pc.u0; ok && n > 0; --n) {
+            for (int n = pc.u1 - pc.u0; ok && n > 0; --n, ++it) {
                 ok = wait(&k_full[s], tiles >> s);
                 tiles ^= 1u << s;
                 const uint64_t kd = kd0 + (uint64_t)s * (L::kTile >> 4);
-                for (int h = 0; ok && h < na; ++h) {
+                for (int x = 0; ok && x < na; ++x) {
+                    const int h = kSplit ? it & 1 : x;
                     if (used) ok = wait(&s_free[buf], par_b);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint64_t qh = qd + (uint64_t)h * (L::kQHalf >> 4);
+                    const uint64_t qh = qd + (uint64_t)x * (L::kQHalf >> 4);
                     if (elect_one()) {
 #pragma unroll
                         for (int kk = 0; kk < D / 16; ++kk)
                             mma_ss(tmem + buf * kUnit, qh + ((kk >> 2) * (kRows * 128) + (kk & 3) * 32 >> 4),
                                    kd + ((kk >> 2) * (kUnit * 128) + (kk & 3) * 32 >> 4), idesc_s, kk > 0);
                         mma_commit(&s_full[4 * h + (turn >> 2 * h & 3)]);
-                        if (h == na - 1) mma_commit(&k_empty[s]);
+                        if (x == na - 1) mma_commit(&k_empty[s]);
                     }
                     __syncwarp();
                     turn = (turn & ~(3u << 2 * h)) | ((turn + (1u << 2 * h)) & (3u << 2 * h));
@@ -313,18 +320,19 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
         constexpr uint32_t idesc_o = idesc<E>(kRows, D, 0, 1);
         const uint64_t pd = smem_desc_sw128(smem_u32(smem + L::kP), 16, 1024);
         const uint64_t vd0 = smem_desc_sw128(smem_u32(smem + L::kVAt), kUnit * 128, 1024);
-        int s = 0;
+        int s = 0, it = 0;
         uint32_t tiles = 0, phase_p = 0;  // bit s: slot s's next tile; bit h: half h's next P
         bool ok = true;
         while (ok && next_piece(a, run, nct, pc, nullptr)) {
             const int rows = group_rows(a, pc.g) - row0;
             if (rows <= 0) continue;
-            const int na = min(NH, (rows + kRows - 1) / kRows);
-            for (int n = 0; ok && n < pc.u1 - pc.u0; ++n) {
+            const int na = kSplit ? 1 : min(NH, (rows + kRows - 1) / kRows);
+            for (int n = 0; ok && n < pc.u1 - pc.u0; ++n, ++it) {
                 ok = wait(&v_full[s], tiles >> s);
                 tiles ^= 1u << s;
                 const uint64_t vd = vd0 + (uint64_t)s * (L::kTile >> 4);
-                for (int h = 0; ok && h < na; ++h) {
+                for (int x = 0; ok && x < na; ++x) {
+                    const int h = kSplit ? it & 1 : x;
                     ok = wait(&p_full[h], phase_p >> h);
                     if (!ok) break;
                     phase_p ^= 1u << h;
@@ -334,9 +342,9 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
 #pragma unroll
                         for (int kk = 0; kk < kUnit / 16; ++kk)
                             mma_ss(tmem + L::kColO + h * D, ph + (kk * 32 >> 4), vd + (kk * 2048 >> 4), idesc_o,
-                                   n > 0 || kk > 0);
+                                   n > (kSplit ? 1 : 0) || kk > 0);
                         mma_commit(&pv_done[h]);
-                        if (h == na - 1) mma_commit(&v_empty[s]);
+                        if (x == na - 1) mma_commit(&v_empty[s]);
                     }
                     __syncwarp();
                 }
@@ -367,13 +375,13 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
         while (next_piece(a, run, nct, pc, half == 0 ? flag0 : nullptr)) {
             const int rows = group_rows(a, pc.g);
             if (row0 >= rows) continue;
-            const int na = min(NH, (rows - row0 + kRows - 1) / kRows), units = pc.u1 - pc.u0;
-            if (half >= na) {
+            const int na = kSplit ? 1 : min(NH, (rows - row0 + kRows - 1) / kRows), units = pc.u1 - pc.u0;
+            if (!kSplit && half >= na) {
                 it += units;
                 job += units * na;
                 continue;
             }
-            const int hrow0 = row0 + half * kRows, row = hrow0 + th, b = pc.g.b;
+            const int hrow0 = row0 + (kSplit ? 0 : half * kRows), row = hrow0 + th, b = pc.g.b;
             const bool live = row < rows, warp_live = hrow0 + (warp & 3) * 32 < rows;
             const int t = a.per_token ? pc.g.tp : row / a.G;
             const int h = pc.hk * a.G + (a.per_token ? row : row % a.G);
@@ -381,8 +389,10 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
             {
                 constexpr int kChunks = D / 8;
                 const int left = min(kRows, rows - hrow0);
+                // kSplit: both halves are done with the last piece's rows and with what they left
+                if (kSplit) asm volatile("bar.sync 1, 256;" ::: "memory");
 #pragma unroll 8
-                for (int i = th; i < kRows * kChunks; i += 128) {
+                for (int i = kSplit ? tid : th; i < kRows * kChunks; i += kSplit ? 256 : 128) {
                     const int r = i / kChunks, c = i % kChunks;
                     uint4 x = make_uint4(0, 0, 0, 0);
                     if (r < left) {
@@ -392,15 +402,17 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
                             static_cast<const char *>(a.q.p) +
                             2 * (b * a.q.sb + hh * a.q.sh + tt * a.q.st) + c * 16);
                     }
-                    *reinterpret_cast<uint4 *>(smem + half * L::kQHalf + (c >> 3) * (kRows * 128) + r * 128 +
+                    *reinterpret_cast<uint4 *>(smem + (kSplit ? 0 : half * L::kQHalf) + (c >> 3) * (kRows * 128) + r * 128 +
                                                (((c & 7) ^ (r & 7)) << 4)) = x;
                 }
                 fence_proxy_async_smem();
-                mbar_arrive(&q_full[half]);
+                mbar_arrive(&q_full[kSplit ? 0 : half]);
             }
             float m = -INFINITY, l = 0.f;
-            job += half;
-            for (int u = pc.u1 - 1; u >= pc.u0; --u, ++it, job += na, ++pv) {
+            bool first = true;  // the accumulator holds nothing of this piece yet
+            if (!kSplit) job += half;
+            for (int u = pc.u1 - 1; u >= pc.u0; --u, ++it, job += na) {
+                if (kSplit && (it & 1) != half) continue;
                 const bool ctx = u < pc.g.ctx_units;
                 uint64_t sees = ~0ull;  // this row's keys of the unit
                 bool masked = false;
@@ -480,7 +492,7 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
                         const float f = mn == -INFINITY ? 1.f : fast_exp2(m - mn);
                         m = mn;
                         l *= f;
-                        if (u != pc.u1 - 1) {  // the accumulator holds this piece's earlier units
+                        if (!first) {
                             tc_fence_after();
 #pragma unroll 1
                             for (int ch = 0; ch < D / 16; ++ch) {
@@ -517,11 +529,42 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&p_full[half]);
+                first = false;
+                ++pv;
             }
             // ---- the piece's end: rows out, or into the workspace
-            job -= half;
-            wait_on(&pv_done[half], pv - 1);
+            if (!kSplit) job -= half;
+            if (pv > 0) wait_on(&pv_done[half], pv - 1);
             tc_fence_after();
+            float f0 = 1.f, f1 = 0.f;  // kSplit: weights of the halves' accumulators
+            float *half1 = reinterpret_cast<float *>(smem);  // [D][128] over Q, which is done with
+            if constexpr (kSplit) {
+                float2 *ml1 = reinterpret_cast<float2 *>(smem + L::kP) + th;  // over P
+                static_assert(NH == 2 && D * kRows * 4 <= L::kP, "room for an accumulator");
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (half == 1) {
+                    *ml1 = make_float2(m, l);
+                    if (warp_live && !first) {
+#pragma unroll 1
+                        for (int ch = 0; ch < D / 32; ++ch) {
+                            uint32_t o[32];
+                            tmem_ld32(acc + ch * 32, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) half1[(ch * 32 + j) * kRows + th] = __uint_as_float(o[j]);
+                        }
+                    }
+                    tc_fence_before();
+                }
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                if (half == 1) continue;
+                const float2 o = *ml1;
+                const float mt = fmaxf(m, o.x);
+                f0 = m == -INFINITY ? 0.f : fast_exp2(m - mt);
+                f1 = o.x == -INFINITY ? 0.f : fast_exp2(o.x - mt);
+                l = (m == -INFINITY ? 0.f : l * f0) + (o.x == -INFINITY ? 0.f : o.y * f1);
+                m = mt;
+            }
             const bool whole = pc.u0 == 0 && pc.u1 == pc.g.units;
             const int item = ((b * a.c.Hk + pc.hk) * a.Tp + pc.g.tp) * a.row_tiles + rt;
             if (tid == 0) {  // half 0 has rows whenever another half has
@@ -529,7 +572,7 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
                 if (pc.u1 == pc.g.units) a.info[item].y = cta;
             }
             const size_t slot = ((size_t)rt * nct + cta) * 2 + (pc.u0 == 0 ? 1 : 0);
-            const size_t prt = slot * (NH * kRows) + half * kRows + th;  // row of the workspace
+            const size_t prt = slot * kTileRows + (kSplit ? 0 : half * kRows) + th;  // row of the workspace
             const size_t orow = ((size_t)b * a.c.Hk * a.G + h) * a.T + t;
             const float inv = !whole ? 1.f : l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
             if (live) {
@@ -547,8 +590,13 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
                     tmem_wait_ld();
                     if (live) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            o[j] = __float_as_uint(l == 0.f ? 0.f : __uint_as_float(o[j]) * inv);
+                        for (int j = 0; j < 32; ++j) {
+                            float x = __uint_as_float(o[j]);
+                            if (kSplit)
+                                x = (f0 != 0.f ? x * f0 : 0.f) +
+                                    (f1 != 0.f ? half1[(ch * 32 + j) * kRows + th] * f1 : 0.f);
+                            o[j] = __float_as_uint(l == 0.f ? 0.f : x * inv);
+                        }
                         if (!whole || a.out_f32) {
                             float *d = whole ? static_cast<float *>(a.out) + orow * D : a.part + prt * D;
                             uint4 *v = reinterpret_cast<uint4 *>(d + ch * 32);
@@ -582,11 +630,11 @@ struct Maps {
     bool fresh;  // kn and vn are there
 };
 
-template <typename E, int D, int NH>
+template <typename E, int D, int NH, bool kSplit>
 cudaError_t launch_one(const CacheAttn &a, int nct, const Maps &m, cudaStream_t st)
 {
     using L = TileSmem<D, NH>;
-    auto kern = cache_tile_kernel<E, D, NH>;
+    auto kern = cache_tile_kernel<E, D, NH, kSplit>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
     if (e != cudaSuccess) return e;
     kern<<<dim3(nct, a.row_tiles), L::kThreads, L::kAlloc, st>>>(a, m.k, m.v, m.kn, m.vn, m.fresh);
@@ -597,9 +645,9 @@ template <typename E, int D>
 cudaError_t launch_halves(const CacheAttn &a, const CacheAttnPlan &p, const Maps &m, cudaStream_t st)
 {
     switch (p.tile_rows / kRows) {
-    case 1: return launch_one<E, D, 1>(a, p.ctas, m, st);
-    case 2: return launch_one<E, D, 2>(a, p.ctas, m, st);
-    default: return launch_one<E, D, 3>(a, p.ctas, m, st);
+    case 1: return launch_one<E, D, 2, true>(a, p.ctas, m, st);
+    case 2: return launch_one<E, D, 2, false>(a, p.ctas, m, st);
+    default: return launch_one<E, D, 3, false>(a, p.ctas, m, st);
     }
 }
 
