@@ -371,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_attn_kernel(const CacheAt
 
 // Joins the parts of rows that several CTAs computed, and writes the rows nobody computed
 // (behind n_tok, or with nothing to see). kWarps warps share a row and take its parts in turn
-// (one warp where a row has few parts: 29 -> {JOIN} us for 20480 rows of 2 or 3 parts; four
+// (one warp where a row has few parts: 29 -> 17 us for 20480 rows of 2 or 3 parts; four
 // where a long row is cut into many). The order of the sums depends on the parts alone.
 template <typename E, int D, int kRowWarps>
 __global__ void __launch_bounds__(128) cache_join_kernel(const CacheAttn a, int tile_rows, int nct, int rows)

@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const ScoreAr
 // CTAs hold the keys of their slots in shared memory, so that happens once. One CTA takes a
 // (sequence, key head) of up to 16384 slots; longer ones take a cluster of CTAs that add
 // their histograms through distributed shared memory (a cluster of two for 4160 slots cost
-// 50 us for 256 heads, its barriers and remote reads, against {KEEP_US} us in one CTA).
+// 50 us for 256 heads, its barriers and remote reads, against 19 us in one CTA).
 // ---------------------------------------------------------------------------------
 constexpr int kKeepBins = 2048;
 constexpr int kKeepSmem = 45 * 1024;  // keys of one CTA held in shared memory (180 KB)
@@ -697,7 +697,7 @@ cudaError_t launch_cache_keep(const CacheKeep &a, cudaStream_t st)
     if (cap <= 16384)
         return launch_cluster(cache_keep_kernel<false, false, 1024>, 1, items, 1024, (size_t)cap * 4, st, a, cap, shift);
     // a CTA per 8192 slots, up to a cluster of 8 (clusters of 16 find room for few at a time:
-    // 430 us against {KEEP_PROMPT} us for 32 heads of 118800 slots)
+    // 430 us against 67 us for 32 heads of 118800 slots)
     int cs = 2;
     while (cs < 8 && cap > 8192 * cs) cs *= 2;
     int held = (cap + cs - 1) / cs;

@@ -7,8 +7,15 @@
 //   warps per half, a thread per row -> P (shared memory) -> O += P V (tensor memory, fp32).
 // S leaves its buffer as soon as a half's threads have loaded it, so two buffers serve three
 // halves (their accumulators fill the other 384 of 512 columns) and every half's threads find
-// their next S waiting. (P written over S instead, the buffer held until the second product:
-// 490 us against {TILE_US} us for a 64-token tree over 8 x 16001..32760 slots, 40 / 8 heads.)
+// their next S waiting. What each step was worth for a 64-token tree over 8 x 16001..32760
+// slots, 40 / 8 heads (320 rows; floor 125 us): P over S's buffer, held until the second
+// product, and one warp for all copies and products 490 us; P in shared memory and four
+// independent warps 387 us; partial units by the copying warps, so that the softmax waits for S
+// alone, 350 us; those by TMA 326 us (626 TFLOP/s). Halves of a second CTA that read K and V
+// again took 537 us. What bounds it now: the chain from S to P of each half (about 2200 cycles
+// of a unit's 3400) and shared memory bandwidth, which the products, P and the copies use to
+// about 60%; fetching units into L2 ahead, spinning waits and cheaper exponentials changed
+// nothing.
 // Units whose 64 keys all exist come by TMA through a map over (d, row, head, page): the page's
 // number is a coordinate, so any strides and page sizes do, and pages of 16 and 32 tokens are 4
 // and 2 boxes of one tile. The others (a sequence's last keys, the new tokens, a tile with an
@@ -79,7 +86,8 @@ struct TileSmem {
 
 // kSplit (NH = 2): the two halves are the same 128 rows, and take every other unit; each has its
 // own running maximum, sum and accumulator, which meet at a piece's end. One half's chain from S
-// to P is then hidden behind the other's (24 rows per key head: {SPLIT_US}).
+// to P is then hidden behind the other's (24 rows per key head: 175 -> 153 us over
+// 8 x 16001..32760 slots, 128 rows 225 -> 169 us).
 template <typename E, int D, int NH, bool kSplit>
 __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
     cache_tile_kernel(const CacheAttn a, const __grid_constant__ CUtensorMap tmK,
