@@ -48,7 +48,8 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_attn_kernel(const CacheAt
     const int cta = blockIdx.x, nct = gridDim.x, rt = blockIdx.y;
     const int page = a.c.page, page_shift = a.page_shift;
 
-    cudaTriggerProgrammaticLaunchCompletion();  // the join may come up and wait
+    cudaGridDependencySynchronize();
+    cudaTriggerProgrammaticLaunchCompletion();  // the join may come up, read the call's inputs and wait
     Run run = find_run<kThreads>(a, sm.run, cta, nct, rt == 0 ? a.flag : nullptr);
     Piece pc;
     while (next_piece(a, run, nct, pc, rt == 0 ? a.flag : nullptr)) {
@@ -386,7 +387,7 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const CacheAttn a, int 
     const int t = rr % a.T, h = (rr / a.T) % (a.c.Hk * a.G), b = rr / a.T / (a.c.Hk * a.G), hk = h / a.G;
     const int tp = a.per_token ? t : 0;
     const int gi = a.idx ? (b * a.c.Hk + hk) * a.Tp + tp : b;
-    const Group gr = load_group(a, gi, nullptr);  // inputs of the call: complete before the first kernel
+    const Group gr = load_group(a, gi, nullptr);  // inputs of the call: there before its first kernel went on
     float o[V], mt = -INFINITY, lt = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) o[v] = 0.f;
@@ -462,9 +463,8 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const CacheAttn a, int 
 template <typename E, int D, int NT, int OCC>
 cudaError_t launch_rows(const CacheAttn &a, int nct, cudaStream_t st)
 {
-    auto kern = cache_attn_kernel<E, D, NT, OCC>;
-    kern<<<dim3(nct, a.row_tiles), kThreads, sizeof(Smem<E, D, NT>), st>>>(a);
-    return cudaGetLastError();
+    return launch_kernel(cache_attn_kernel<E, D, NT, OCC>, dim3(nct, a.row_tiles), kThreads, sizeof(Smem<E, D, NT>),
+                         1, st, a);
 }
 
 template <typename E>
@@ -484,18 +484,8 @@ cudaError_t launch_join(const CacheAttn &a, const CacheAttnPlan &p, cudaStream_t
     const int rows = a.c.B * a.c.Hk * a.G * a.T;
     // a row's parts, about: the CTAs of its row tile over the rows of work they share
     const bool few = p.ctas / (a.c.B * a.c.Hk * a.Tp) <= 8;
-    // programmatic launch: the join's CTAs start while the last units end and wait there
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(few ? (rows + 3) / 4 : rows);
-    cfg.blockDim = dim3(128);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, few ? cache_join_kernel<E, D, 1> : cache_join_kernel<E, D, 4>, a, p.tile_rows,
-                              p.ctas, rows);
+    return launch_kernel(few ? cache_join_kernel<E, D, 1> : cache_join_kernel<E, D, 4>,
+                         dim3(few ? (rows + 3) / 4 : rows), 128, 0, 1, st, a, p.tile_rows, p.ctas, rows);
 }
 
 bool strides_map(const ab_cache &c)

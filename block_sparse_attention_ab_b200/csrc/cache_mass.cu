@@ -73,6 +73,7 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_mass_kernel(const CacheMa
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int page = a.c.page, page_shift = a.page_shift;
 
+    cudaGridDependencySynchronize();
     // ---- this CTA's run of units
     const int per = (a.c.B + kThreads - 1) / kThreads;
     auto units_of = [&](int b, int *flag) {
@@ -306,14 +307,9 @@ cudaError_t launch_one(const CacheMass &a, cudaStream_t st)
     int rows = a.G * a.T;
     if (rows > kRows) rows = kRows;
     const int smem = (int)(sizeof(Smem<D>) + (size_t)((rows + 7) / 8) * (D / 32) * 32 * 16);
-    if (smem > 48 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-    }
     int occ = 220 * 1024 / (smem + 1024);  // CTAs per SM that the shared memory leaves room for
     if (occ > OCC) occ = OCC;
-    kern<<<kCacheSms * occ, kThreads, smem, st>>>(a);
-    return cudaGetLastError();
+    return launch_kernel(kern, dim3(kCacheSms * occ), kThreads, smem, 1, st, a);
 }
 
 template <typename E>

@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_alloc(tmem_slot, 512);
         tmem_relinquish();
     }
+    cudaGridDependencySynchronize();
     // ---- this CTA's run of units, in order of sequences and key heads
     int *flag0 = blockIdx.x == 0 ? a.flag : nullptr;
     auto units_of = [&](int b, int *flag) {
@@ -375,11 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <typename E, int D>
 cudaError_t launch_one(const CacheMass &a, const CUtensorMap &tk, cudaStream_t st)
 {
-    auto kern = cache_mass_tile_kernel<E, D>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, MassSmem<D>::kAlloc);
-    if (e != cudaSuccess) return e;
-    kern<<<kCacheSms, kThreads, MassSmem<D>::kAlloc, st>>>(a, tk);
-    return cudaGetLastError();
+    return launch_kernel(cache_mass_tile_kernel<E, D>, dim3(kCacheSms), kThreads, MassSmem<D>::kAlloc, 1, st, a, tk);
 }
 
 }  // namespace

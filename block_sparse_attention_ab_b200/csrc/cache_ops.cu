@@ -72,6 +72,7 @@ __global__ void __launch_bounds__(kPageThreads) cache_append_kernel(const Append
 {
     using Sum = PageSum<D>;
     __shared__ __align__(16) float sm[Sum::kGroups * D];
+    cudaGridDependencySynchronize();
     const int b = blockIdx.z, hk = blockIdx.y, tid = threadIdx.x;
     const bool first = blockIdx.x == 0 && hk == 0;
     int *flag = first && tid == 0 ? a.flag : nullptr;
@@ -167,6 +168,7 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const ScoreAr
 {
     constexpr int V = D / 32;  // float4s per lane
     extern __shared__ __align__(16) float sm[];
+    cudaGridDependencySynchronize();
     cg::cluster_group cl = cg::this_cluster();
     const int cs = cl.num_blocks(), rank = cl.block_rank();
     const int item = blockIdx.x / cs;
@@ -349,6 +351,7 @@ __global__ void __launch_bounds__(kThreads, kFar ? 1 : 2) cache_keep_kernel(cons
     __shared__ int sm_warp[32];
     __shared__ int sm_digit, sm_above;
     __shared__ int3 sm_cnt;  // this CTA's keys equal to the threshold, holes, movers
+    cudaGridDependencySynchronize();
     cg::cluster_group cl = cg::this_cluster();
     const int cs = kCluster ? cl.num_blocks() : 1, rank = kCluster ? cl.block_rank() : 0, tid = threadIdx.x;
     auto sync = [&]() {
@@ -533,6 +536,7 @@ __global__ void __launch_bounds__(kPageThreads, 10)
     using Sum = PageSum<D>;
     __shared__ __align__(16) float sm[Sum::kGroups * D];
     __shared__ int sm_page[128], sm_row[128];  // pool page and row of each row's source
+    cudaGridDependencySynchronize();
     const int lp = blockIdx.x, hk = blockIdx.y, b = blockIdx.z, tid = threadIdx.x;
     const int page = c.page, cap = c.max_pages << page_shift;
     const bool first = lp == 0 && hk == 0 && tid == 0;
@@ -601,29 +605,6 @@ __global__ void __launch_bounds__(kPageThreads, 10)
 
 int shift_of(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
 
-template <typename K, typename... A>
-cudaError_t launch_cluster(K kern, int cs, int blocks, int threads, size_t smem, cudaStream_t st, A... args)
-{
-    cudaError_t e = cudaSuccess;
-    if (smem > 48 * 1024)
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess && cs > 8)
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = cs;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
 }  // namespace
 
 cudaError_t launch_cache_append(const ab_cache &c, const ab_tokens &k, const ab_tokens &v, int T,
@@ -634,25 +615,11 @@ cudaError_t launch_cache_append(const ab_cache &c, const ab_tokens &k, const ab_
     // T tokens touch at most this many pages, wherever they start
     const dim3 grid((T - 1) / c.page + 2, c.Hk, c.B);
     const bool h = c.dtype == AB_F16;
-    if (c.d == 64) {
-        if (h) cache_append_kernel<Fp16, 64><<<grid, kPageThreads, 0, st>>>(a);
-        else cache_append_kernel<Bf16, 64><<<grid, kPageThreads, 0, st>>>(a);
-    } else {
-        if (h) cache_append_kernel<Fp16, 128><<<grid, kPageThreads, 0, st>>>(a);
-        else cache_append_kernel<Bf16, 128><<<grid, kPageThreads, 0, st>>>(a);
-    }
-    cudaError_t e = cudaGetLastError();
+    auto kern = c.d == 64 ? (h ? cache_append_kernel<Fp16, 64> : cache_append_kernel<Bf16, 64>)
+                          : (h ? cache_append_kernel<Fp16, 128> : cache_append_kernel<Bf16, 128>);
+    const cudaError_t e = launch_kernel(kern, grid, kPageThreads, 0, 1, st, a);
     if (e != cudaSuccess || start) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((c.B + 127) / 128);
-    cfg.blockDim = dim3(128);
-    cfg.stream = st;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, cache_length_kernel, a);
+    return launch_kernel(cache_length_kernel, dim3((c.B + 127) / 128), 128, 0, 1, st, a);
 }
 
 cudaError_t launch_cache_score(const ab_cache &c, const ab_tokens &q, int G, int T,
@@ -687,7 +654,7 @@ cudaError_t launch_cache_score(const ab_cache &c, const ab_tokens &q, int G, int
     const bool h = c.dtype == AB_F16;
     auto kern = c.d == 64 ? (h ? page_score_kernel<Fp16, 64> : page_score_kernel<Bf16, 64>)
                           : (h ? page_score_kernel<Fp16, 128> : page_score_kernel<Bf16, 128>);
-    return launch_cluster(kern, cs, items * cs, kScoreThreads, smem, st, a);
+    return launch_kernel(kern, dim3(items * cs), kScoreThreads, smem, cs, st, a);
 }
 
 cudaError_t launch_cache_keep(const CacheKeep &a, cudaStream_t st)
@@ -695,7 +662,7 @@ cudaError_t launch_cache_keep(const CacheKeep &a, cudaStream_t st)
     const int cap = a.c.max_pages * a.c.page, items = a.c.B * a.c.Hk;
     const int shift = shift_of(a.c.page);
     if (cap <= 16384)
-        return launch_cluster(cache_keep_kernel<false, false, 1024>, 1, items, 1024, (size_t)cap * 4, st, a, cap, shift);
+        return launch_kernel(cache_keep_kernel<false, false, 1024>, dim3(items), 1024, (size_t)cap * 4, 1, st, a, cap, shift);
     // a CTA per 8192 slots, up to a cluster of 8 (clusters of 16 find room for few at a time:
     // 430 us against 67 us for 32 heads of 118800 slots)
     int cs = 2;
@@ -703,7 +670,7 @@ cudaError_t launch_cache_keep(const CacheKeep &a, cudaStream_t st)
     int held = (cap + cs - 1) / cs;
     if (held > kKeepSmem) held = kKeepSmem;
     auto kern = held * cs < cap ? cache_keep_kernel<true, true, 1024> : cache_keep_kernel<true, false, 1024>;
-    return launch_cluster(kern, cs, items * cs, 1024, (size_t)held * 4, st, a, held, shift);
+    return launch_kernel(kern, dim3(items * cs), 1024, (size_t)held * 4, cs, st, a, held, shift);
 }
 
 cudaError_t launch_cache_compact(const ab_cache &c, int budget, const int32_t *src,
@@ -714,8 +681,7 @@ cudaError_t launch_cache_compact(const ab_cache &c, int budget, const int32_t *s
     const bool h = c.dtype == AB_F16;
     auto kern = c.d == 64 ? (h ? cache_compact_kernel<Fp16, 64> : cache_compact_kernel<Bf16, 64>)
                           : (h ? cache_compact_kernel<Fp16, 128> : cache_compact_kernel<Bf16, 128>);
-    kern<<<grid, kPageThreads, 0, st>>>(c, budget, shift_of(c.page), src, n_keep, flag);
-    return cudaGetLastError();
+    return launch_kernel(kern, grid, kPageThreads, 0, 1, st, c, budget, shift_of(c.page), src, n_keep, flag);
 }
 
 }  // namespace ab

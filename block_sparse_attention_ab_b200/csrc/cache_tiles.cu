@@ -112,7 +112,6 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
     const int row0 = rt * kTileRows;
     const int page = a.c.page, shift = a.page_shift;
 
-    cudaTriggerProgrammaticLaunchCompletion();  // the join may come up and wait
     if (tid == 0) {
         for (int s = 0; s < L::kSlots; ++s) {
             mbar_init(&k_full[s], 1);   // and v_full behind it
@@ -135,6 +134,8 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
         tmem_alloc(tmem_slot, L::kTmemCols);
         tmem_relinquish();
     }
+    cudaGridDependencySynchronize();
+    cudaTriggerProgrammaticLaunchCompletion();  // the join may come up, read the call's inputs and wait
     int *flag0 = rt == 0 ? a.flag : nullptr;  // one report per bad length or count
     Run run = find_run<L::kThreads>(a, run_sm, cta, nct, flag0);
     tc_fence_before();
@@ -642,11 +643,8 @@ template <typename E, int D, int NH, bool kSplit>
 cudaError_t launch_one(const CacheAttn &a, int nct, const Maps &m, cudaStream_t st)
 {
     using L = TileSmem<D, NH>;
-    auto kern = cache_tile_kernel<E, D, NH, kSplit>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kAlloc);
-    if (e != cudaSuccess) return e;
-    kern<<<dim3(nct, a.row_tiles), L::kThreads, L::kAlloc, st>>>(a, m.k, m.v, m.kn, m.vn, m.fresh);
-    return cudaGetLastError();
+    return launch_kernel(cache_tile_kernel<E, D, NH, kSplit>, dim3(nct, a.row_tiles), L::kThreads, L::kAlloc, 1, st, a,
+                         m.k, m.v, m.kn, m.vn, m.fresh);
 }
 
 template <typename E, int D>
