@@ -7,7 +7,9 @@
 // the query rows' fragments (up to 256 rows) and log-sums lie in shared memory, in the
 // fragment's own order, so a step is one 16-byte shared load per lane for two products. A
 // key's sum over rows stays in one warp: no atomics, and the same bits for equal calls. The
-// CTAs take equal runs of 64-key units of the sequences' heads in order.
+// CTAs take equal runs of 64-key units of the sequences' heads in order. Bound by reading K: 16
+// sequences of 1023..32760 slots, 40 / 8 heads: 102 us, 5.6 TB/s. Three CTAs per SM took 114 us,
+// five (spilling) 144. More than 8 rows without a plan go to cache_mass_tiles.cu.
 #include <cstdint>
 
 #include "cache_common.cuh"

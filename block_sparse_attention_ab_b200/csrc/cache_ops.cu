@@ -57,7 +57,8 @@ struct PageSum {
 
 // ---------------------------------------------------------------------------------
 // ab_cache_append: one CTA per (page that receives a token, key head, sequence). The page's
-// older keys are read once more for its sum; every new row is read and written once.
+// older keys are read once more for its sum; every new row is read and written once. Bound by
+// that for a prompt (49140 tokens of 12 heads: 108 us, 5.7 TB/s), by the launch for a token.
 // ---------------------------------------------------------------------------------
 struct AppendArgs {
     ab_cache c;
@@ -145,7 +146,9 @@ __global__ void cache_length_kernel(const AppendArgs a)
 // (sequence, key head[, token]); each CTA keeps its pages' logits in shared memory, the
 // clusters exchange row maxima and sums through distributed shared memory, so one launch
 // reads every sum once and writes every score once. Eight lanes share a page; a warp has
-// 8 pages (4 KB at d = 128) in flight.
+// 8 pages (4 KB at d = 128) in flight. 32 sequences of 4097..32760 slots in pages of 16, 40 / 8
+// heads: 42 us, 3.6 TB/s: the longest clusters' chain of phases. Clusters twice as large took 53
+// us, one CTA each 66, half the pages in flight 67, twice as many 43.
 // ---------------------------------------------------------------------------------
 constexpr int kScoreThreads = 256;
 constexpr int kScoreLanes = 8;
@@ -526,7 +529,8 @@ __global__ void __launch_bounds__(kThreads, kFar ? 1 : 2) cache_keep_kernel(cons
 // slots >= n_keep to slots < n_keep only, so no CTA writes what another one reads. A page
 // that changed is read whole for its sum. Bound by the moved rows (read and written once) and
 // those sums; the first threads look the rows' sources up, so that every row's loads are
-// independent.
+// independent. 256 heads with 64 of 4096 slots to fill: 38 us for 170 MB of changed pages; 32
+// heads, 0.33 GB of moves: 73 us.
 // ---------------------------------------------------------------------------------
 template <typename E, int D>
 __global__ void __launch_bounds__(kPageThreads, 10)
