@@ -812,3 +812,51 @@ def test_one_token_of_a_full_table_and_of_many_sequences():
     ref, rel = score(many, q)
     assert ab.check_flag(flag) == 0
     assert bool(((sc.cpu().to(F64) - ref).abs() <= rel * ref + 1e-30).all())
+
+
+def test_captured_behind_copies_and_a_second_stream():
+    """The calls' launches overlap the kernel before them; in a graph that may be a copy, a
+    fill, or the join of two streams."""
+    c = HostCache([200, 31], 2, 64, 32, BF, spare=12, max_pages=9, seed=91)
+    for b in range(2):
+        c.allocate(b, 288)
+    g = c.to_gpu()
+    src = [x.cuda() for x in (c.randn(2, 4, 2, 64), c.randn(2, 2, 2, 64), c.randn(2, 2, 2, 64))]
+    q, k, v = (torch.empty_like(t) for t in src)
+    start = g.length.clone()
+    mass_out = torch.empty_like(g.mass)
+
+    def step():
+        q.copy_(src[0])  # a memory copy
+        cur, other = torch.cuda.current_stream(), torch.cuda.Stream()
+        other.wait_stream(cur)
+        with torch.cuda.stream(other):
+            k.copy_(src[1])
+            v.copy_(src[2])
+            mass_out.zero_()
+        cur.wait_stream(other)
+        out, lse = ab.cache_attn(g, q, k, v, want_lse=True)
+        other.wait_stream(cur)
+        with torch.cuda.stream(other):
+            ab.cache_append(g, k, v, start=start)
+            ab.cache_mass(g, q, lse, out=mass_out)
+        cur.wait_stream(other)
+        return out, lse
+
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        ref = [t.clone() for t in step()] + [mass_out.clone()]
+        g.length.copy_(start)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        out, lse = step()
+    for _ in range(3):
+        for t in (q, k, v, out, lse, mass_out):
+            t.fill_(7)
+        g.length.copy_(start)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((out, lse, mass_out), ref):
+            assert torch.equal(a, b)
+        assert torch.equal(g.length, start + 2)
