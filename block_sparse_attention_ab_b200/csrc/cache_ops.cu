@@ -301,9 +301,9 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const ScoreAr
 // fp32 bits, which order as the values do for values >= 0), then one ordered pass that
 // ranks holes and movers. Bound by one read of scores and positions (8 bytes per slot); its
 // CTAs hold the keys of their slots in shared memory, so that happens once. One CTA takes a
-// (sequence, key head) of up to 16384 slots; longer ones take a cluster of CTAs that add
-// their histograms through distributed shared memory (a cluster of two for 4160 slots cost
-// 50 us for 256 heads, its barriers and remote reads, against 19 us in one CTA).
+// (sequence, key head); long ones take a cluster of CTAs that add their histograms through
+// distributed shared memory (launch_cache_keep has the rule and its figures). 256 heads of 4160
+// slots: 19 us in one CTA each, 50 in clusters of two.
 // ---------------------------------------------------------------------------------
 constexpr int kKeepBins = 2048;
 constexpr int kKeepSmem = 45 * 1024;  // keys of one CTA held in shared memory (180 KB)
@@ -533,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, kFar ? 1 : 2) cache_keep_kernel(cons
 // heads, 0.33 GB of moves: 73 us.
 // ---------------------------------------------------------------------------------
 template <typename E, int D>
-__global__ void __launch_bounds__(kPageThreads, 10)
+__global__ void __launch_bounds__(kPageThreads, 8)
     cache_compact_kernel(const ab_cache c, int budget, int page_shift, const int32_t *src_all,
                          const int32_t *n_keep, int *flag)
 {
@@ -665,12 +665,16 @@ cudaError_t launch_cache_keep(const CacheKeep &a, cudaStream_t st)
 {
     const int cap = a.c.max_pages * a.c.page, items = a.c.B * a.c.Hk;
     const int shift = shift_of(a.c.page);
-    if (cap <= 16384)
-        return launch_kernel(cache_keep_kernel<false, false, 1024>, dim3(items), 1024, (size_t)cap * 4, 1, st, a, cap, shift);
-    // a CTA per 8192 slots, up to a cluster of 8 (clusters of 16 find room for few at a time:
-    // 430 us against 67 us for 32 heads of 118800 slots)
-    int cs = 2;
-    while (cs < 8 && cap > 8192 * cs) cs *= 2;
+    // As few CTAs as hold a head's keys (36864 each), because a cluster's barriers and remote
+    // histograms cost more than they share out; up to four where the GPU would stand empty. 128
+    // heads of 32760 slots: 34 us in one CTA each, 41 in two, 71 in four; 32 heads of 118800: 43
+    // in four, 69 in eight; 32 heads of 60000: 29 in four, 38 in two.
+    int cs = 1;
+    while (cs < 8 && cap > 36864 * cs) cs *= 2;
+    while (cs < 4 && cap > 8192 * cs && items * cs * 2 <= kCacheSms) cs *= 2;
+    if (cs == 1)
+        return launch_kernel(cache_keep_kernel<false, false, 1024>, dim3(items), 1024, (size_t)cap * 4, 1, st, a, cap,
+                             shift);
     int held = (cap + cs - 1) / cs;
     if (held > kKeepSmem) held = kKeepSmem;
     auto kern = held * cs < cap ? cache_keep_kernel<true, true, 1024> : cache_keep_kernel<true, false, 1024>;
