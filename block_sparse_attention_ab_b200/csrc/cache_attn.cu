@@ -372,15 +372,17 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_attn_kernel(const CacheAt
 }
 
 // Joins the parts of rows that several CTAs computed, and writes the rows nobody computed
-// (behind n_tok, or with nothing to see). kWarps warps share a row and take its parts in turn
-// (one warp where a row has few parts: 29 -> 17 us for 20480 rows of 2 or 3 parts; four
-// where a long row is cut into many). The order of the sums depends on the parts alone.
+// (behind n_tok, or with nothing to see). kRowWarps warps share a row and take its parts in
+// turn: one where a row has few (29 -> 17 us for 20480 rows of 2 or 3 parts), four, or sixteen
+// where a long row is cut into very many. The order of the sums depends on the parts alone.
+constexpr int join_threads(int row_warps) { return row_warps > 4 ? 32 * row_warps : 128; }
+
 template <typename E, int D, int kRowWarps>
-__global__ void __launch_bounds__(128) cache_join_kernel(const CacheAttn a, int tile_rows, int nct, int rows)
+__global__ void __launch_bounds__(join_threads(kRowWarps)) cache_join_kernel(const CacheAttn a, int tile_rows, int nct, int rows)
 {
-    constexpr int kPer = 4 / kRowWarps;  // rows of a CTA
-    constexpr int V = D / 32;            // values per lane
-    __shared__ float sm_m[4], sm_l[4], sm_o[4][D];
+    constexpr int kPer = join_threads(kRowWarps) / 32 / kRowWarps;  // rows of a CTA
+    constexpr int V = D / 32;                                      // values per lane
+    __shared__ float sm_m[kRowWarps], sm_l[kRowWarps], sm_o[kRowWarps][D];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % kRowWarps;
     const int row = blockIdx.x * kPer + warp / kRowWarps;
     const bool exists = row < rows;
@@ -405,8 +407,9 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const CacheAttn a, int 
         write = who.x != who.y;  // else one CTA had it all and wrote it
         const int parts = write ? who.y - who.x + 1 : 0;
         // 32 parts at a time: their maxima and weights by lane, then their rows, whose loads do
-        // not wait for one another (one part after the other: 72 us against {LONG} us for one
-        // sequence of 100000 slots with one key head, whose rows have 444 parts)
+        // not wait for one another (one part after the other: 72 us against 32 us for a
+        // call on one sequence of 100000 slots with one key head, whose rows have 444 parts;
+        // sixteen warps a row instead of four then 22 us)
         const size_t slot0 = ((size_t)rt * nct + who.x) * 2;
         for (int base = 0; sub + kRowWarps * base < parts; base += 32) {
             auto row_at = [&](int k) {  // row n of part sub + kRowWarps k
@@ -453,12 +456,14 @@ __global__ void __launch_bounds__(128) cache_join_kernel(const CacheAttn a, int 
         for (int v = 0; v < V; ++v) sm_o[warp][lane * V + v] = o[v];
         __syncthreads();
         if (warp != 0) return;
-        mt = fmaxf(fmaxf(sm_m[0], sm_m[1]), fmaxf(sm_m[2], sm_m[3]));
+        mt = sm_m[0];
+#pragma unroll
+        for (int w = 1; w < kRowWarps; ++w) mt = fmaxf(mt, sm_m[w]);
         lt = 0.f;
 #pragma unroll
         for (int v = 0; v < V; ++v) o[v] = 0.f;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < kRowWarps; ++w) {
             if (sm_m[w] == -INFINITY) continue;
             const float f = fast_exp2(sm_m[w] - mt);
             lt += sm_l[w] * f;
@@ -505,7 +510,11 @@ cudaError_t launch_join(const CacheAttn &a, const CacheAttnPlan &p, cudaStream_t
 {
     const int rows = a.c.B * a.c.Hk * a.G * a.T;
     // a row's parts, about: the CTAs of its row tile over the rows of work they share
-    const bool few = p.ctas / (a.c.B * a.c.Hk * a.Tp) <= 8;
+    const int parts = p.ctas / (a.c.B * a.c.Hk * a.Tp);
+    if (parts > 64)
+        return launch_kernel(cache_join_kernel<E, D, 16>, dim3(rows), join_threads(16), 0, 1, st, a, p.tile_rows,
+                             p.ctas, rows);
+    const bool few = parts <= 8;
     return launch_kernel(few ? cache_join_kernel<E, D, 1> : cache_join_kernel<E, D, 4>,
                          dim3(few ? (rows + 3) / 4 : rows), 128, 0, 1, st, a, p.tile_rows, p.ctas, rows);
 }
