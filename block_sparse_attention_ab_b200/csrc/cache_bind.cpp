@@ -247,11 +247,13 @@ Tensor mass(const Cache &x, const Tensor &q, const Tensor &lse, const OptTensor 
 py::tuple keep(const Cache &x, int64_t budget, int64_t recent, const OptTensor &next_pos, const OptTensor &score,
                const OptTensor &pos, const OptTensor &length, const OptTensor &workspace, const OptTensor &dev_flag)
 {
-    if (budget > INT32_MAX || recent > INT32_MAX) bad_value("budget or recent is too large");
+    // before they are cut to the 32 bits of the C ABI: src is allocated from the whole budget
+    if (budget < 1 || budget > INT32_MAX) bad_value("budget must be 1 .. 2^31 - 1");
+    if (recent < 0 || recent > INT32_MAX) bad_value("recent must be 0 .. 2^31 - 1");
     const int64_t B = x.c.B, Hk = x.c.Hk;
     const std::array<int64_t, 3> slots = {x.c.n_pages, Hk, x.c.page};
     Cache::On on(x.dev);
-    Tensor src = x.empty({B, Hk, std::max<int64_t>(budget, 0)}, at::kInt), n = x.empty({B}, at::kInt);
+    Tensor src = x.empty({B, Hk, budget}, at::kInt), n = x.empty({B}, at::kInt);
     size_t need = 0;
     check(ab_cache_keep_workspace_size(x.c, (int)budget, &need), "ab_cache_keep");
     Tensor ws = workspace ? *workspace : x.empty({(int64_t)need}, at::kByte);
