@@ -491,7 +491,7 @@ template <typename E, int D, int NT, int OCC>
 cudaError_t launch_rows(const CacheAttn &a, int nct, cudaStream_t st)
 {
     return launch_kernel(cache_attn_kernel<E, D, NT, OCC>, dim3(nct, a.row_tiles), kThreads, sizeof(Smem<E, D, NT>),
-                         1, st, a);
+                         sizeof(Smem<E, D, NT>), 1, st, a);
 }
 
 template <typename E>
@@ -512,11 +512,11 @@ cudaError_t launch_join(const CacheAttn &a, const CacheAttnPlan &p, cudaStream_t
     // a row's parts, about: the CTAs of its row tile over the rows of work they share
     const int parts = p.ctas / (a.c.B * a.c.Hk * a.Tp);
     if (parts > 64)
-        return launch_kernel(cache_join_kernel<E, D, 16>, dim3(rows), join_threads(16), 0, 1, st, a, p.tile_rows,
+        return launch_kernel(cache_join_kernel<E, D, 16>, dim3(rows), join_threads(16), 0, 0, 1, st, a, p.tile_rows,
                              p.ctas, rows);
     const bool few = parts <= 8;
     return launch_kernel(few ? cache_join_kernel<E, D, 1> : cache_join_kernel<E, D, 4>,
-                         dim3(few ? (rows + 3) / 4 : rows), 128, 0, 1, st, a, p.tile_rows, p.ctas, rows);
+                         dim3(few ? (rows + 3) / 4 : rows), 128, 0, 0, 1, st, a, p.tile_rows, p.ctas, rows);
 }
 
 bool strides_map(const ab_cache &c)

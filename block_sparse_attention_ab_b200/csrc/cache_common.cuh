@@ -174,12 +174,19 @@ __device__ __forceinline__ void qk_product(float (&s)[4], const uint4 (&kr)[2][D
 // serialization: its CTAs may come up while the kernel before it ends, so every kernel launched
 // here waits (cudaGridDependencySynchronize) before it reads or writes global memory. That takes
 // 1 to 2 us off each of a step's short kernels.
+// `smem_most`: the most dynamic shared memory that this kernel is ever launched with. A kernel's
+// limit is state of the process that all its calls share, so every call that sets it sets this
+// same value: two threads' calls cannot lower it under one another, nor a later call under a
+// captured one. The default limit of 48 KB holds for static and dynamic memory together; the
+// kernels here have kMostStatic bytes of static memory at most.
+constexpr size_t kMostStatic = 12 * 1024;
 template <typename... P, typename... A>
-cudaError_t launch_kernel(void (*kern)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t st,
-                          A... args)
+cudaError_t launch_kernel(void (*kern)(P...), dim3 grid, int threads, size_t smem, size_t smem_most, int cluster,
+                          cudaStream_t st, A... args)
 {
     cudaError_t e = cudaSuccess;
-    if (smem > 48 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (smem > 48 * 1024 - kMostStatic)
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_most);
     if (e == cudaSuccess && cluster > 8)
         e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;

@@ -308,10 +308,11 @@ cudaError_t launch_one(const CacheMass &a, cudaStream_t st)
     auto kern = cache_mass_kernel<E, D, OCC>;
     int rows = a.G * a.T;
     if (rows > kRows) rows = kRows;
-    const int smem = (int)(sizeof(Smem<D>) + (size_t)((rows + 7) / 8) * (D / 32) * 32 * 16);
+    auto bytes = [](int tiles) { return (int)(sizeof(Smem<D>) + (size_t)tiles * (D / 32) * 32 * 16); };
+    const int smem = bytes((rows + 7) / 8);
     int occ = 220 * 1024 / (smem + 1024);  // CTAs per SM that the shared memory leaves room for
     if (occ > OCC) occ = OCC;
-    return launch_kernel(kern, dim3(kCacheSms * occ), kThreads, smem, 1, st, a);
+    return launch_kernel(kern, dim3(kCacheSms * occ), kThreads, smem, bytes(kRows / 8), 1, st, a);
 }
 
 template <typename E>

@@ -376,7 +376,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <typename E, int D>
 cudaError_t launch_one(const CacheMass &a, const CUtensorMap &tk, cudaStream_t st)
 {
-    return launch_kernel(cache_mass_tile_kernel<E, D>, dim3(kCacheSms), kThreads, MassSmem<D>::kAlloc, 1, st, a, tk);
+    return launch_kernel(cache_mass_tile_kernel<E, D>, dim3(kCacheSms), kThreads, MassSmem<D>::kAlloc,
+                         MassSmem<D>::kAlloc, 1, st, a, tk);
 }
 
 }  // namespace

@@ -307,6 +307,7 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const ScoreAr
 // ---------------------------------------------------------------------------------
 constexpr int kKeepBins = 2048;
 constexpr int kKeepSmem = 45 * 1024;  // keys of one CTA held in shared memory (180 KB)
+static_assert((kKeepBins + 64) * sizeof(int) <= kMostStatic, "the histogram and the scans' words");
 
 // The key of a slot at index `at` of score and pos: order of the score, +inf when recent.
 __device__ __forceinline__ uint32_t keep_key(float x, int pos, int recent, int limit, int *flag)
@@ -621,9 +622,9 @@ cudaError_t launch_cache_append(const ab_cache &c, const ab_tokens &k, const ab_
     const bool h = c.dtype == AB_F16;
     auto kern = c.d == 64 ? (h ? cache_append_kernel<Fp16, 64> : cache_append_kernel<Bf16, 64>)
                           : (h ? cache_append_kernel<Fp16, 128> : cache_append_kernel<Bf16, 128>);
-    const cudaError_t e = launch_kernel(kern, grid, kPageThreads, 0, 1, st, a);
+    const cudaError_t e = launch_kernel(kern, grid, kPageThreads, 0, 0, 1, st, a);
     if (e != cudaSuccess || start) return e;
-    return launch_kernel(cache_length_kernel, dim3((c.B + 127) / 128), 128, 0, 1, st, a);
+    return launch_kernel(cache_length_kernel, dim3((c.B + 127) / 128), 128, 0, 0, 1, st, a);
 }
 
 cudaError_t launch_cache_score(const ab_cache &c, const ab_tokens &q, int G, int T,
@@ -650,7 +651,7 @@ cudaError_t launch_cache_score(const ab_cache &c, const ab_tokens &q, int G, int
     while (cs < 16 && ((items * cs < 2 * kCacheSms && c.max_pages >= 64 * cs) || c.max_pages > 2048 * cs)) cs *= 2;
     a.slice = (c.max_pages + cs - 1) / cs;
     const int rows = per_token ? G : G * T;
-    const size_t room = 160 * 1024 - (size_t)a.slice * 8;
+    const size_t most = 160 * 1024, room = most - (size_t)a.slice * 8;
     a.chunk = (int)(room / ((size_t)a.slice * 4 + c.d * 4 + 16));
     if (a.chunk > 32) a.chunk = 32;
     if (a.chunk > rows) a.chunk = rows;
@@ -658,7 +659,7 @@ cudaError_t launch_cache_score(const ab_cache &c, const ab_tokens &q, int G, int
     const bool h = c.dtype == AB_F16;
     auto kern = c.d == 64 ? (h ? page_score_kernel<Fp16, 64> : page_score_kernel<Bf16, 64>)
                           : (h ? page_score_kernel<Fp16, 128> : page_score_kernel<Bf16, 128>);
-    return launch_kernel(kern, dim3(items * cs), kScoreThreads, smem, cs, st, a);
+    return launch_kernel(kern, dim3(items * cs), kScoreThreads, smem, most, cs, st, a);
 }
 
 cudaError_t launch_cache_keep(const CacheKeep &a, cudaStream_t st)
@@ -673,12 +674,12 @@ cudaError_t launch_cache_keep(const CacheKeep &a, cudaStream_t st)
     while (cs < 8 && cap > 36864 * cs) cs *= 2;
     while (cs < 4 && cap > 8192 * cs && items * cs * 2 <= kCacheSms) cs *= 2;
     if (cs == 1)
-        return launch_kernel(cache_keep_kernel<false, false, 1024>, dim3(items), 1024, (size_t)cap * 4, 1, st, a, cap,
-                             shift);
+        return launch_kernel(cache_keep_kernel<false, false, 1024>, dim3(items), 1024, (size_t)cap * 4, kKeepSmem * 4,
+                             1, st, a, cap, shift);
     int held = (cap + cs - 1) / cs;
     if (held > kKeepSmem) held = kKeepSmem;
     auto kern = held * cs < cap ? cache_keep_kernel<true, true, 1024> : cache_keep_kernel<true, false, 1024>;
-    return launch_kernel(kern, dim3(items * cs), 1024, (size_t)held * 4, cs, st, a, held, shift);
+    return launch_kernel(kern, dim3(items * cs), 1024, (size_t)held * 4, kKeepSmem * 4, cs, st, a, held, shift);
 }
 
 cudaError_t launch_cache_compact(const ab_cache &c, int budget, const int32_t *src,
@@ -689,7 +690,7 @@ cudaError_t launch_cache_compact(const ab_cache &c, int budget, const int32_t *s
     const bool h = c.dtype == AB_F16;
     auto kern = c.d == 64 ? (h ? cache_compact_kernel<Fp16, 64> : cache_compact_kernel<Bf16, 64>)
                           : (h ? cache_compact_kernel<Fp16, 128> : cache_compact_kernel<Bf16, 128>);
-    return launch_kernel(kern, grid, kPageThreads, 0, 1, st, c, budget, shift_of(c.page), src, n_keep, flag);
+    return launch_kernel(kern, grid, kPageThreads, 0, 0, 1, st, c, budget, shift_of(c.page), src, n_keep, flag);
 }
 
 }  // namespace ab

@@ -645,8 +645,8 @@ template <typename E, int D, int NH, bool kSplit>
 cudaError_t launch_one(const CacheAttn &a, int nct, const Maps &m, cudaStream_t st)
 {
     using L = TileSmem<D, NH>;
-    return launch_kernel(cache_tile_kernel<E, D, NH, kSplit>, dim3(nct, a.row_tiles), L::kThreads, L::kAlloc, 1, st, a,
-                         m.k, m.v, m.kn, m.vn, m.fresh);
+    return launch_kernel(cache_tile_kernel<E, D, NH, kSplit>, dim3(nct, a.row_tiles), L::kThreads, L::kAlloc, L::kAlloc, 1,
+                         st, a, m.k, m.v, m.kn, m.vn, m.fresh);
 }
 
 template <typename E, int D>

@@ -36,6 +36,60 @@ def _i32(*x):
     return torch.tensor(x, dtype=torch.int32, device="cuda")
 
 
+_KEEP_ALONE = """
+import sys
+import torch
+import block_sparse_attention_ab_b200 as ab
+from cache_reference import HostCache, keep
+Hk, slots = int(sys.argv[1]), int(sys.argv[2])
+c = HostCache([slots], Hk, 64, 16, torch.bfloat16, seed=1, max_pages=slots // 16)
+src, n = ab.cache_keep(c.to_gpu(), slots // 3)
+ref, m = keep(c, slots // 3)
+assert torch.equal(src.cpu(), ref) and torch.equal(n.cpu(), m)
+print("kept")
+"""
+
+
+@pytest.mark.parametrize("Hk,slots", [(1, 45056), (40, 22528), (80, 11264)])
+def test_keep_alone_in_a_process(Hk, slots):
+    """Keys that fit the default limit of shared memory, but not beside the kernel's own arrays:
+    no larger call has raised the limit before."""
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([os.path.dirname(HERE), HERE]))
+    out = subprocess.run([sys.executable, "-c", _KEEP_ALONE, str(Hk), str(slots)], env=env, capture_output=True,
+                         text=True, timeout=300)
+    assert out.returncode == 0 and "kept" in out.stdout, out.stderr[-2000:]
+
+
+def test_keep_of_two_sizes_from_two_threads():
+    """Calls that need different amounts of shared memory, made by two host threads at once."""
+    from block_sparse_attention_ab_b200.cache import AB_BF16, CacheStruct
+    L = ab.lib()
+    made = []
+    for slots in (29696, 15360):  # 119 and 60 KB of keys
+        pages = slots // 128
+        held = torch.rand(pages, 148, 128, device="cuda"), torch.arange(pages, device="cuda").int(), _i32(slots)
+        src, n, ws = (torch.zeros(m, dtype=torch.int32, device="cuda") for m in (14800, 1, 14800))
+        s = CacheStruct(None, None, None, held[0].data_ptr(), None, held[1].data_ptr(), held[2].data_ptr(), 0, 0, 0, 0,
+                        0, 0, 1, 148, 64, 128, pages, pages, AB_BF16)
+        made.append((s, src, n, ws, torch.cuda.Stream(), held))
+    torch.cuda.synchronize()
+    codes = [set(), set()]
+
+    def calls(i):
+        s, src, n, ws, stream, _ = made[i]
+        for _ in range(1500):
+            codes[i].add(L.ab_cache_keep(s, 100, 0, None, None, None, None, src.data_ptr(), n.data_ptr(),
+                                         ws.data_ptr(), ws.numel() * 4, None, stream.cuda_stream))
+
+    threads = [threading.Thread(target=calls, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert codes == [{0}, {0}]
+
+
 def test_keep_refuses_sizes_outside_32_bits():
     g = HostCache([40], 1, 64, 16, BF, seed=17).to_gpu()
     for budget in (0, -1, 5 - 2 ** 32, -2 ** 31 - 1, 2 ** 32 + 5, 2 ** 62):
