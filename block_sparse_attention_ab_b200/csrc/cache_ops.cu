@@ -57,7 +57,8 @@ struct PageSum {
 
 // ---------------------------------------------------------------------------------
 // ab_cache_append: one CTA per (page that receives a token, key head, sequence). The page's
-// older keys are read once more for its sum; every new row is read and written once. Bound by
+// older keys are read once more for its sum; every new row is read and written once. A sequence
+// that is cut inside a page and receives nothing has that page's sum made anew too. Bound by
 // that for a prompt (49140 tokens of 12 heads: 108 us, 5.7 TB/s), by the launch for a token.
 // ---------------------------------------------------------------------------------
 struct AppendArgs {
@@ -88,7 +89,7 @@ __global__ void __launch_bounds__(kPageThreads) cache_append_kernel(const Append
     if (n < n_ask) raise_flag(flag, AB_FLAG_CACHE_FULL);
     if (first && tid == 0 && a.start) a.c.length[b] = len;
     const int lp = s0 / page + blockIdx.x;
-    if (n == 0 || lp * page >= len) return;
+    if (lp * page >= len || (n == 0 && !(a.start && a.c.ksum))) return;
     const int pg = cache_page(a.c, b, lp, a.flag);
     if (pg < 0) return;
     const int rows = min(page, len - lp * page), lane = tid % Sum::kLanes;

@@ -463,8 +463,8 @@ typedef struct {
 /*
  * ab_cache_append -- write the keys and values of new tokens into the cache. Token i of
  * sequence b (i < n_new[b]) comes from row sel[b][i] of k, v and goes to slot start[b] + i,
- * with mass 0 and position pos0[b] + i; the ksum of every page that received a token is
- * recomputed; length[b] = start[b] + n_new[b].
+ * with mass 0 and position pos0[b] + i; the ksum of every page that received a token, and of
+ * the page that start[b] lies inside of, is recomputed; length[b] = start[b] + n_new[b].
  * k, v   : [B, Hk, T, d] of the cache's type. T: 1 .. 2^20.
  * n_new  : int32 [B], or NULL for T each.
  * sel    : int32 [B, T], or NULL for rows 0, 1, 2, ...: the accepted tokens of a drafted

@@ -90,6 +90,32 @@ def test_keep_of_two_sizes_from_two_threads():
     assert codes == [{0}, {0}]
 
 
+@pytest.mark.parametrize("page,d,dtype", [(16, 64, FP), (128, 128, BF)])
+def test_rollback_that_adds_nothing(page, d, dtype):
+    """Every drafted token of a sequence taken back: sums and scores are those of a cache that
+    never held them."""
+    def fresh():
+        c = HostCache([0, 0, 0], 2, d, page, dtype, spare=12, max_pages=4, seed=3)
+        for b in range(3):
+            c.allocate(b, 4 * page)
+        return c, c.to_gpu()
+    c, a = fresh()
+    _, e = fresh()
+    k, v = c.randn(3, 2, 3 * page, d).cuda(), c.randn(3, 2, 3 * page, d).cuda()
+    at = [page + 5, 2 * page, 2 * page + 1]  # in a page, at a page's end, one slot into a page
+    ab.cache_append(a, k, v)
+    flag, held = _flag(), (a.k.clone(), a.v.clone())
+    ab.cache_append(a, v, k, n_new=_i32(0, 0, 0), start=_i32(*at), dev_flag=flag)
+    ab.cache_append(e, k, v, n_new=_i32(*at))
+    assert ab.check_flag(flag) == 0 and a.length.tolist() == e.length.tolist() == at
+    for b in range(3):
+        pages = c.table[b, : -(-at[b] // page)].long().cuda()
+        assert torch.equal(a.ksum[pages], e.ksum[pages])
+    assert torch.equal(a.k, held[0]) and torch.equal(a.v, held[1])
+    q = c.randn(3, 4, 1, d).cuda()
+    assert torch.equal(ab.cache_score(a, q), ab.cache_score(e, q))
+
+
 def test_keep_refuses_sizes_outside_32_bits():
     g = HostCache([40], 1, 64, 16, BF, seed=17).to_gpu()
     for budget in (0, -1, 5 - 2 ** 32, -2 ** 31 - 1, 2 ** 32 + 5, 2 ** 62):
