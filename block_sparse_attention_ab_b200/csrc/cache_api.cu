@@ -51,6 +51,13 @@ ab_status check_written(const ab_cache &c)
                : AB_ERR_UNSUPPORTED;
 }
 
+// An array that a call writes while its other CTAs read `in` must not share memory with it.
+bool overlap(const int32_t *out, size_t n_out, const int32_t *in, size_t n_in)
+{
+    const uintptr_t o = reinterpret_cast<uintptr_t>(out), i = reinterpret_cast<uintptr_t>(in);
+    return out && in && o < i + 4 * n_in && i < o + 4 * n_out;
+}
+
 ab_status check_tokens(const ab_tokens &t)
 {
     if (!t.p) return AB_ERR_NULL;
@@ -99,7 +106,12 @@ ab_status ab_cache_append(ab_cache c, ab_tokens k, ab_tokens v, int T, const int
     AB_TRY(check_tokens(k));
     AB_TRY(check_tokens(v));
     if (!aligned(n_new, 4) || !aligned(sel, 4) || !aligned(start, 4) || !aligned(pos0, 4)) return AB_ERR_ALIGN;
-    if (start == c.length) return AB_ERR_UNSUPPORTED;  // read by some CTAs while one writes it
+    // with start, one CTA writes a sequence's length while the others read these; without it a
+    // kernel behind the first one adds n_new to length, sequence by sequence
+    if (start && (overlap(c.length, c.B, start, c.B) || overlap(c.length, c.B, n_new, c.B) ||
+                  overlap(c.length, c.B, pos0, c.B) || overlap(c.length, c.B, sel, (size_t)c.B * T)))
+        return AB_ERR_UNSUPPORTED;
+    if (!start && n_new != c.length && overlap(c.length, c.B, n_new, c.B)) return AB_ERR_UNSUPPORTED;
     return ab::status_of(ab::launch_cache_append(c, k, v, T, n_new, sel, start, pos0, dev_flag,
                                                  (cudaStream_t)stream));
 }

@@ -470,10 +470,13 @@ typedef struct {
  * sel    : int32 [B, T], or NULL for rows 0, 1, 2, ...: the accepted tokens of a drafted
  *          tree, for instance. A row outside 0 .. T - 1 raises AB_FLAG_BAD_INDEX and is
  *          written as zeros.
- * start  : int32 [B] (not the cache's length array), or NULL to append at length. With it
- *          the sequence is cut or kept at start[b] first: slots from start[b] + n_new[b]
- *          on are no longer valid.
- * pos0   : int32 [B], or NULL for start.
+ * start  : int32 [B], or NULL to append at length. With it the sequence is cut or kept at
+ *          start[b] first: slots from start[b] + n_new[b] on are no longer valid. With it
+ *          start, n_new, sel and pos0 must not lie in the cache's length array, which the
+ *          call writes while it reads them (AB_ERR_UNSUPPORTED); give copies of it.
+ * pos0   : int32 [B], or NULL for start (a token's position is its slot, which holds while
+ *          no slot has been evicted).
+ * The new tokens' k and v must not lie in rows of the cache that the call writes.
  * Tokens that do not fit into max_pages * page slots are dropped (AB_FLAG_CACHE_FULL). A
  * start outside 0 .. max_pages * page raises AB_FLAG_BAD_INDEX and leaves the sequence as
  * it is.

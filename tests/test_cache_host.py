@@ -157,3 +157,14 @@ def test_new_flag_bit_is_its_own():
     bits = [ab.FLAG_BAD_SCORE, ab.FLAG_BAD_INDEX, ab.FLAG_BAD_WEIGHT, ab.FLAG_TIMEOUT, ab.FLAG_SCHED_COLLISION,
             ab.FLAG_CACHE_FULL]
     assert bits == [1, 2, 4, 8, 16, 32]
+
+
+def test_append_refuses_arrays_in_the_length_it_writes(L):
+    """With start, length is written while the other arrays are read; parts of it too."""
+    c = cache(length=P + 4096)  # B = 3: 12 bytes
+    far = dict(n_new=P, sel=P + 64, start=P + 256, pos0=P + 512)
+    for name in far:
+        for at in (P + 4096, P + 4100, P + 4104, P + 4088):
+            assert append(L, c, **{**far, name: at}) == UNSUPPORTED, (name, at)
+    # at the sequence's end a second kernel reads n_new and writes length, each at its sequence
+    assert append(L, c, **{**far, "start": None, "n_new": P + 4100}) == UNSUPPORTED

@@ -116,6 +116,30 @@ def test_rollback_that_adds_nothing(page, d, dtype):
     assert torch.equal(ab.cache_score(a, q), ab.cache_score(e, q))
 
 
+def test_append_with_the_length_array():
+    """length as start, position or count beside start is refused: the call writes it. Copies of
+    it, and length as the count without start, do what they say."""
+    c = HostCache([70, 33, 5], 4, 64, 16, BF, spare=30, seed=20, max_pages=10)
+    for b in range(3):
+        c.allocate(b, 160)
+    g = c.to_gpu()
+    k, v = c.randn(3, 4, 70, 64).cuda(), c.randn(3, 4, 70, 64).cuda()
+    old = g.length.clone()
+    for bad in (dict(start=g.length), dict(start=old, pos=g.length), dict(start=old, n_new=g.length)):
+        with pytest.raises(ab.AbError, match="UNSUPPORTED"):
+            ab.cache_append(g, k, v, **bad)
+    assert torch.equal(g.length, old)
+    ab.cache_append(g, k[:, :, :40], v[:, :, :40], start=old, pos=old.clone())
+    assert torch.equal(g.length, old + 40)
+    for b in range(3):
+        s = torch.arange(int(old[b]), int(old[b]) + 40)
+        pg = c.table[b, s // 16].long().cuda()
+        assert torch.equal(g.pos[pg, :, (s % 16).cuda()].cpu(), s.int().unsqueeze(1).expand(-1, 4))
+    g.length.copy_(old)
+    ab.cache_append(g, k, v, n_new=g.length)
+    assert torch.equal(g.length, 2 * old)
+
+
 def test_keep_refuses_sizes_outside_32_bits():
     g = HostCache([40], 1, 64, 16, BF, seed=17).to_gpu()
     for budget in (0, -1, 5 - 2 ** 32, -2 ** 31 - 1, 2 ** 32 + 5, 2 ** 62):
