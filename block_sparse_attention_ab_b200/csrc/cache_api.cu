@@ -246,6 +246,11 @@ ab_status ab_cache_keep(ab_cache c, int budget, int recent, const int32_t *next_
         !aligned(src, 4) || !aligned(n_keep, 4) || !aligned(workspace, 4))
         return AB_ERR_ALIGN;
     if (!workspace || workspace_bytes < need) return AB_ERR_WORKSPACE;
+    if (!length) length = c.length;
+    const size_t n_src = (size_t)c.B * c.Hk * budget;
+    if (overlap(n_keep, c.B, length, c.B) || overlap(src, n_src, length, c.B) ||
+        (recent > 0 && (overlap(n_keep, c.B, next_pos, c.B) || overlap(src, n_src, next_pos, c.B))))
+        return AB_ERR_UNSUPPORTED;  // written by one head's CTA while the others read them
     ab::CacheKeep a = {};
     a.c = c;
     a.budget = budget;
@@ -253,7 +258,7 @@ ab_status ab_cache_keep(ab_cache c, int budget, int recent, const int32_t *next_
     a.next_pos = next_pos;
     a.score = score;
     a.pos = pos;
-    a.length = length ? length : c.length;
+    a.length = length;
     a.src = src;
     a.n_keep = n_keep;
     a.movers = static_cast<int32_t *>(workspace);

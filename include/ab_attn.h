@@ -571,7 +571,8 @@ ab_status ab_cache_mass(ab_cache c, ab_tokens q, int Hq, int T, const int32_t *n
  *            raises AB_FLAG_BAD_SCORE and counts as 0.
  * pos      : int32 [n_pages, Hk, page], NULL for the cache's; not read when recent is 0.
  * length   : int32 [B], NULL for the cache's. next_pos: int32 [B] (required when recent > 0).
- * src      : out, int32 [B, Hk, budget]. n_keep: out, int32 [B]: m.
+ * src      : out, int32 [B, Hk, budget]. n_keep: out, int32 [B]: m. Neither may share memory
+ *            with length or next_pos (AB_ERR_UNSUPPORTED); ab_cache_compact sets length.
  * workspace: ab_cache_keep_workspace_size() bytes.
  */
 ab_status ab_cache_keep_workspace_size(ab_cache c, int budget, size_t *bytes);

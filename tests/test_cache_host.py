@@ -168,3 +168,16 @@ def test_append_refuses_arrays_in_the_length_it_writes(L):
             assert append(L, c, **{**far, name: at}) == UNSUPPORTED, (name, at)
     # at the sequence's end a second kernel reads n_new and writes length, each at its sequence
     assert append(L, c, **{**far, "start": None, "n_new": P + 4100}) == UNSUPPORTED
+
+
+def test_keep_refuses_outputs_over_its_inputs(L):
+    """n_keep and src are written by one head while the others read length and next_pos."""
+    c = cache(length=P + 4096)  # B = 3, Hk = 2: src has 600 words
+    far = dict(src=P + 32768, n_keep=P + 65536, next_pos=P + 8192, recent=1)
+    for at in (P + 4096, P + 4100, P + 4088, P + 8192, P + 8200):
+        assert keep(L, c, **{**far, "n_keep": at}) == UNSUPPORTED
+    for at in (P + 4096, P + 4096 - 2396, P + 8200, P + 8192 - 4):
+        assert keep(L, c, **{**far, "src": at}) == UNSUPPORTED
+    # the length given in place of the cache's
+    assert L.ab_cache_keep(c, 100, 0, None, None, None, P + 65536, P + 32768, P + 65540, P, 1 << 40, None, None) == \
+        UNSUPPORTED
