@@ -275,7 +275,9 @@ ab_status ab_cache_compact(ab_cache c, int budget, const int32_t *src, const int
     if (!src || !n_keep) return AB_ERR_NULL;
     if (budget < 1 || budget > 1 << 30) return AB_ERR_RANGE;
     if (!aligned(src, 4) || !aligned(n_keep, 4)) return AB_ERR_ALIGN;
-    if (n_keep == c.length) return AB_ERR_UNSUPPORTED;  // read by some CTAs while one writes it
+    // read by some CTAs while one writes length
+    if (overlap(c.length, c.B, n_keep, c.B) || overlap(c.length, c.B, src, (size_t)c.B * c.Hk * budget))
+        return AB_ERR_UNSUPPORTED;
     return ab::status_of(ab::launch_cache_compact(c, budget, src, n_keep, dev_flag, (cudaStream_t)stream));
 }
 

@@ -586,7 +586,7 @@ ab_status ab_cache_keep(ab_cache c, int budget, int recent, const int32_t *next_
  * src[b][hk][j] go to slot j < n_keep[b]; the ksum of pages that changed, and of the last
  * page where it is not full, is recomputed; length[b] = n_keep[b]. An entry below n_keep[b]
  * that is neither j nor a slot >= n_keep[b] inside the table raises AB_FLAG_BAD_INDEX and
- * is not moved.
+ * is not moved. src and n_keep must not lie in the length array (AB_ERR_UNSUPPORTED).
  */
 ab_status ab_cache_compact(ab_cache c, int budget, const int32_t *src, const int32_t *n_keep,
                            int *dev_flag, void *stream);

@@ -181,3 +181,11 @@ def test_keep_refuses_outputs_over_its_inputs(L):
     # the length given in place of the cache's
     assert L.ab_cache_keep(c, 100, 0, None, None, None, P + 65536, P + 32768, P + 65540, P, 1 << 40, None, None) == \
         UNSUPPORTED
+
+
+def test_compact_refuses_arrays_in_the_length_it_writes(L):
+    c = cache(length=P + 4096)  # B = 3
+    for at in (P + 4096, P + 4104, P + 4088):
+        assert compact(L, c, src=P + 32768, n_keep=at) == UNSUPPORTED
+    for at in (P + 4096, P + 4104, P + 4096 - 2396):
+        assert compact(L, c, src=at, n_keep=P + 65536) == UNSUPPORTED
