@@ -115,6 +115,8 @@ struct Cache {
             bad_value(std::string(name) + " must be [" + std::to_string(c.B) + ", " +
                       (heads < 0 ? "Hq" : std::to_string(heads)) + ", T, " + std::to_string(c.d) + "], got " +
                       shape_of(t.sizes()));
+        if (t.size(1) > INT32_MAX || t.size(2) > INT32_MAX)  // the C ABI's counts have 32 bits
+            bad_value(std::string(name) + " has too many heads or tokens");
         if (t.stride(3) != 1) bad_value(std::string(name) + ": rows must be contiguous");
         auto st = [&](int i) { return t.size(i) > 1 ? t.stride(i) : (int64_t)0; };
         return {t.data_ptr(), st(0), st(1), st(2)};
@@ -161,7 +163,6 @@ void append(const Cache &x, const Tensor &k, const Tensor &v, const OptTensor &n
 {
     const ab_tokens tk = x.tokens(k, x.c.Hk, "k"), tv = x.tokens(v, x.c.Hk, "v");
     if (v.size(2) != k.size(2)) bad_value("k and v must have one shape");
-    if (k.size(2) > INT32_MAX) bad_value("too many tokens");
     const int T = (int)k.size(2);
     Cache::On on(x.dev);
     check(ab_cache_append(x.c, tk, tv, T, x.per_seq(n_new, "n_new"),

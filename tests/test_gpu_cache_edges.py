@@ -148,3 +148,17 @@ def test_keep_refuses_sizes_outside_32_bits():
     for recent in (-1, 5 - 2 ** 32, 2 ** 32 + 5):
         with pytest.raises((ValueError, ab.AbError)):
             ab.cache_keep(g, 8, recent=recent, next_pos=_i32(40))
+
+
+def test_sizes_past_32_bits_are_refused():
+    c = HostCache([40], 1, 64, 16, BF, spare=4, seed=52)
+    g = c.to_gpu()
+    for shape in ((1, 2 ** 32 + 2, 1, 64), (1, 2, 2 ** 32 + 1, 64)):
+        q = torch.zeros(1, 1, 1, 64, dtype=BF, device="cuda").expand(shape)
+        with pytest.raises(ValueError, match="too many"):
+            ab.cache_score(g, q, per_token=False)
+        with pytest.raises(ValueError, match="too many"):
+            ab.cache_mass(g, q, torch.zeros(1, 2, 1, device="cuda"))
+    k = torch.zeros(1, 1, 1, 64, dtype=BF, device="cuda").expand(1, 1, 2 ** 32 + 1, 64)
+    with pytest.raises(ValueError, match="too many"):
+        ab.cache_append(g, k, k)
