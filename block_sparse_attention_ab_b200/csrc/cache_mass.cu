@@ -82,8 +82,12 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_mass_kernel(const CacheMa
         const int len = cache_len(a.c, a.c.length, b, flag);
         return (long long)((len + kUnit - 1) / kUnit) * a.c.Hk;
     };
+    int *flag0 = blockIdx.x ? nullptr : a.flag;  // one CTA reports the bad lengths and counts, of every sequence
     long long mine = 0;
-    for (int b = tid * per; b < min((tid + 1) * per, a.c.B); ++b) mine += units_of(b, blockIdx.x ? nullptr : a.flag);
+    for (int b = tid * per; b < min((tid + 1) * per, a.c.B); ++b) {
+        mine += units_of(b, flag0);
+        if (flag0) tok_count(a.n_tok, b, a.T, flag0);
+    }
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -126,7 +130,7 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_mass_kernel(const CacheMa
         }
         const int hk = (int)(in_group / units), u0 = (int)(in_group % units);
         const int u1 = (int)min((long long)units, u0 + left);
-        const int n = min(tok_count(a.n_tok, b, a.T, blockIdx.x ? nullptr : a.flag), len);
+        const int n = min(tok_count(a.n_tok, b, a.T, nullptr), len);
         const int old_len = len - n, rows = n * a.G;
         const char *kbase = static_cast<const char *>(a.c.k) + 2 * hk * a.c.k_head;
         const bool per_row = a.idx && a.per_token;

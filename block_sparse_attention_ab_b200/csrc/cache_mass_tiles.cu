@@ -95,13 +95,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     cudaGridDependencySynchronize();
     // ---- this CTA's run of units, in order of sequences and key heads
-    int *flag0 = blockIdx.x == 0 ? a.flag : nullptr;
+    int *flag0 = blockIdx.x == 0 ? a.flag : nullptr;  // one CTA reports the bad lengths and counts
     auto units_of = [&](int b, int *flag) {
         return (cache_len(a.c, a.c.length, b, flag) + kKeys - 1) / kKeys;
     };
     const int per = (a.c.B + kThreads - 1) / kThreads;
     long long mine = 0;
-    for (int b = tid * per; b < min((tid + 1) * per, a.c.B); ++b) mine += (long long)units_of(b, flag0) * a.c.Hk;
+    for (int b = tid * per; b < min((tid + 1) * per, a.c.B); ++b) {
+        mine += (long long)units_of(b, flag0) * a.c.Hk;
+        if (flag0) tok_count(a.n_tok, b, a.T, flag0);
+    }
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -139,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     int run_b = lo < hi ? found[0] : 0;
     long long in_group = lo < hi ? *reinterpret_cast<long long *>(found + 2) : 0, left = hi - lo;
-    auto next_piece = [&](Piece &p, int *flag) -> bool {
+    auto next_piece = [&](Piece &p) -> bool {
         while (left > 0) {
             p.len = cache_len(a.c, a.c.length, run_b, nullptr);
             const int units = (p.len + kKeys - 1) / kKeys;
@@ -152,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             p.hk = (int)(in_group / units);
             p.u0 = (int)(in_group % units);
             p.u1 = (int)min((long long)units, p.u0 + left);
-            p.n = min(tok_count(a.n_tok, p.b, a.T, flag), p.len);
+            p.n = min(tok_count(a.n_tok, p.b, a.T, nullptr), p.len);
             left -= p.u1 - p.u0;
             in_group += p.u1 - p.u0;
             return true;
@@ -171,7 +174,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int it = 0, s = 0;
         uint32_t par_e = 1, phase = 0, loaded = 0;
         bool ok = true;
-        while (ok && next_piece(pc, nullptr)) {
+        while (ok && next_piece(pc)) {
             const int slots = (pc.len + page - 1) >> shift, rows = pc.n * a.G;
             for (int r0 = 0; ok && r0 < rows; r0 += kRows) {
                 const int batch = 32 / nent;  // units whose pages are looked up together
@@ -226,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int it = 0, s = 0;
         uint32_t tiles = 0, q = 0;
         bool ok = true;
-        while (ok && next_piece(pc, nullptr)) {
+        while (ok && next_piece(pc)) {
             const int rows = pc.n * a.G;
             for (int r0 = 0; ok && r0 < rows; r0 += kRows) {
                 const uint32_t id = idesc<E>(kKeys, (min(kRows, rows - r0) + 31) & ~31, 0, 0);
@@ -265,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         bool ok = true;
         int it = 0;
-        while (next_piece(pc, flag0)) {
+        while (next_piece(pc)) {
             const int rows = pc.n * a.G, old_len = pc.len - pc.n;
             if (rows == 0) {  // nothing to add: the masses as they are
                 if (a.out != a.c.mass)

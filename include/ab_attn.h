@@ -542,8 +542,8 @@ ab_status ab_cache_attn(ab_cache c, ab_tokens q, ab_tokens k, ab_tokens v, int H
 
 /*
  * ab_cache_mass -- add the attention weight that every slot received from a sequence's
- * newest tokens, after those were appended. With n = n_tok[b] of them, the i-th (row
- * sel[b][i] of q and lse, or row i) sees slots s < length[b] - n + i + 1:
+ * newest tokens, after those were appended. With n = n_tok[b] of them (length[b] where that is
+ * less), the i-th (row sel[b][i] of q and lse, or row i) sees slots s < length[b] - n + i + 1:
  *   mass_out[s] = mass[s] + sum_{h in group, i} w e^{q_{h,i}.k_s/sqrt(d) - lse_{h,i}}.
  * q, lse   : what ab_cache_attn was given and returned ([B, Hq, T, d], fp32 [B, Hq, T]
  *            contiguous). sel: int32 [B, T] or NULL; a row outside 0 .. T - 1 raises

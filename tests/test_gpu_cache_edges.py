@@ -162,3 +162,20 @@ def test_sizes_past_32_bits_are_refused():
     k = torch.zeros(1, 1, 1, 64, dtype=BF, device="cuda").expand(1, 1, 2 ** 32 + 1, 64)
     with pytest.raises(ValueError, match="too many"):
         ab.cache_append(g, k, k)
+
+
+@pytest.mark.parametrize("T", [1, 16])  # the kernel for few rows, and that for many
+@pytest.mark.parametrize("bad", [-1, 1000])
+def test_mass_reports_counts_of_every_sequence(T, bad):
+    c = HostCache([70, 300, 0, 200], 2, 64, 32, BF, seed=12)
+    q, lse = c.randn(4, 4, T, 64).cuda(), 5 + torch.rand(4, 4, T, generator=c.g).cuda()
+    for b in range(4):
+        n = [T] * 4
+        n[b] = bad
+        for x, bits in ((n, ab.FLAG_BAD_INDEX), ([min(max(i, 0), T) for i in n], 0)):
+            g, flag = c.to_gpu(), _flag()
+            ab.cache_mass(g, q, lse, n_tok=_i32(*x), dev_flag=flag)
+            assert ab.check_flag(flag) == bits, (b, x)
+            if bits:
+                got = g.mass
+        assert torch.equal(got, g.mass)  # clamped
