@@ -258,17 +258,20 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_mass_kernel(const CacheMa
                             for (int i = 0; i < DI; ++i) qf[i] = sm.q[(nt * DI + i) * 32 + lane];
                             qk_product<E, DI>(s, kc, qf);
                             const float2 l2 = *reinterpret_cast<const float2 *>(&sm.lse2[nt * 8 + 2 * c]);
-                            float x0 = fmaf(s[0], a.scale_log2, sh0 - l2.x);
-                            float x1 = fmaf(s[1], a.scale_log2, sh0 - l2.y);
-                            float x2 = fmaf(s[2], a.scale_log2, sh1 - l2.x);
-                            float x3 = fmaf(s[3], a.scale_log2, sh1 - l2.y);
+                            float a0 = sh0 - l2.x, a1 = sh0 - l2.y, a2 = sh1 - l2.x, a3 = sh1 - l2.y;
                             if (per_row) {
                                 const int k0 = min(n - 1, (r0 + nt * 8 + 2 * c) / a.G);
                                 const int k1 = min(n - 1, (r0 + nt * 8 + 2 * c + 1) / a.G);
                                 const float h0 = rsh[k0], h1 = rsh[k1];
-                                if (key < old_len) x0 += h0, x1 += h1;
-                                if (key + 8 < old_len) x2 += h0, x3 += h1;
+                                if (key < old_len) a0 += h0, a1 += h1;
+                                if (key + 8 < old_len) a2 += h0, a3 += h1;
                             }
+                            // -inf: the row does not exist, saw nothing, or its plan has no such
+                            // page; then nothing comes of a logit that is infinite or NaN either
+                            float x0 = a0 == -INFINITY ? a0 : fmaf(s[0], a.scale_log2, a0);
+                            float x1 = a1 == -INFINITY ? a1 : fmaf(s[1], a.scale_log2, a1);
+                            float x2 = a2 == -INFINITY ? a2 : fmaf(s[2], a.scale_log2, a2);
+                            float x3 = a3 == -INFINITY ? a3 : fmaf(s[3], a.scale_log2, a3);
                             if (edge) {
                                 const int2 bd = *reinterpret_cast<const int2 *>(&sm.bound[nt * 8 + 2 * c]);
                                 if (key >= bd.x) x0 = -INFINITY;

@@ -47,7 +47,8 @@ struct MassSmem {
     // k_full, k_empty [kSlots], s_full, s_free [2], q_full, drain
     static constexpr int kNumBars = 2 * kSlots + 6;
     static constexpr int kMisc = kBars + kNumBars * 8;  // tensor memory address, abort flag, run
-    static constexpr int kBytes = kMisc + 16 + 18 * 8 + 16;
+    static constexpr int kVoid = kMisc + 16 + 18 * 8 + 16;  // some row of these 32 adds nothing [kRows / 32]
+    static constexpr int kBytes = kVoid + kRows / 32 * 4;
     static constexpr int kAlloc = kBytes + 1024;
     // info slot i is rewritten for unit i + kInfos, whose tile waits for the product of unit i +
     // kInfos - kSlots, which waits until the sets have read buffers (and info) of two units before
@@ -64,6 +65,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint8_t *smem = align_smem_1024(smem_raw);
     float *nlse = reinterpret_cast<float *>(smem + L::kLse);
     int *bound = reinterpret_cast<int *>(smem + L::kBound);
+    int *voids = reinterpret_cast<int *>(smem + L::kVoid);
     float *part = reinterpret_cast<float *>(smem + L::kPart);
     TileInfo *info = reinterpret_cast<TileInfo *>(smem + L::kInfo);
     uint64_t *k_full = reinterpret_cast<uint64_t *>(smem + L::kBars), *k_empty = k_full + NS;
@@ -289,8 +291,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int k = r / a.G, t = a.sel ? a.sel[(size_t)pc.b * a.T + k] : k;
                     return (unsigned)t < (unsigned)a.T ? t : -1;
                 };
-                for (int i = tid; i < np; i += kSums) {
-                    const int r = r0 + i, t = row_of(r);
+                static_assert(kRows <= kSums, "a thread per row");
+                if (tid < np) {  // whole warps: np is a multiple of 32
+                    const int r = r0 + tid, t = row_of(r);
                     float nl = -INFINITY;
                     if (t >= 0) {
                         const int h = pc.hk * a.G + r % a.G;
@@ -299,8 +302,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                     } else if (r < rows) {
                         raise_flag(a.flag, AB_FLAG_BAD_INDEX);
                     }
-                    nlse[i] = nl;
-                    bound[i] = r < rows ? old_len + r / a.G + 1 : 0;
+                    // a row that does not exist or saw nothing adds nothing, whatever its logit
+                    const bool none = nl == -INFINITY;
+                    nlse[tid] = nl;
+                    bound[tid] = none ? 0 : old_len + r / a.G + 1;
+                    const bool some = __any_sync(~0u, none);
+                    if (lane == 0) voids[warp] = some;
                 }
                 constexpr int kChunks = D / 8;
 #pragma unroll 4
@@ -334,6 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     const bool edge = (u + 1) * kKeys > old_len;
                     for (int c0 = 32 * half; c0 < np; c0 += 64) {
+                        const bool masked = edge || voids[c0 >> 5];
                         uint32_t x[32];
                         tmem_ld32(tmem + lanes + set * kRows + c0, x);
                         tmem_wait_ld();
@@ -344,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                           fmaf(__uint_as_float(x[j + 1]), a.scale_log2, nl.y),
                                           fmaf(__uint_as_float(x[j + 2]), a.scale_log2, nl.z),
                                           fmaf(__uint_as_float(x[j + 3]), a.scale_log2, nl.w)};
-                            if (edge) {
+                            if (masked) {
                                 const int4 bd = *reinterpret_cast<const int4 *>(bound + c0 + j);
                                 if (key >= bd.x) y[0] = -INFINITY;
                                 if (key >= bd.y) y[1] = -INFINITY;

@@ -179,3 +179,59 @@ def test_mass_reports_counts_of_every_sequence(T, bad):
             if bits:
                 got = g.mass
         assert torch.equal(got, g.mass)  # clamped
+
+
+def _mass_of(c, q, lse, n_tok=None, plan=(None, None, None)):
+    g = c.to_gpu()
+    idx, cnt, w = (None if t is None else t.cuda() for t in plan)
+    ab.cache_mass(g, q.cuda(), lse.cuda(), n_tok=n_tok, idx=idx, cnt=cnt, w=w)
+    return g.mass.cpu()
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+@pytest.mark.parametrize("T", [1, 3])
+@pytest.mark.parametrize("page,d", [(16, 64), (128, 128)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_mass_outside_a_plan_takes_no_part(rows, T, page, d, bad):
+    """NaN and infinity in the keys of a page that no row's plan has, and of slots below the new
+    tokens in their page."""
+    if rows not in (1, T):
+        pytest.skip("a plan has one row, or one per token")
+    L = 3 * page + 9
+    c = HostCache([L], 2, d, page, BF, seed=13)
+    q, lse = c.randn(1, 4, T, d), 5 + torch.rand(1, 4, T, generator=c.g)
+    idx = torch.full((1, 2, rows, c.max_pages), -1, dtype=torch.int32)
+    idx[..., 0], idx[..., 1] = 0, 2
+    cnt = torch.full((1, 2, rows), 2, dtype=torch.int32)
+    plan = (idx, cnt, torch.full(idx.shape, 2.0))
+    ref = _mass_of(c, q, lse, plan=plan)
+    c.k[c.table[0, 1].long()] = bad
+    c.k[c.table[0, 3].long(), :, : 9 - T] = bad
+    assert torch.equal(_mass_of(c, q, lse, plan=plan), ref)
+
+
+@pytest.mark.parametrize("G,T", [(1, 1), (3, 1), (3, 15), (5, 60)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+def test_mass_of_infinite_keys(G, T, dtype):
+    """A key whose logit is -inf for every row gets nothing; a row that saw nothing (its log-sum
+    is -inf) and a row that does not exist add nothing, to a key whose logit is +inf or NaN for it
+    either."""
+    c = HostCache([500, 40], 1, 64, 64, dtype, seed=14)
+    q, lse = c.randn(2, G, T, 64), 5 + torch.rand(2, G, T, generator=c.g)
+    q[..., 0] = -q[..., 0].abs() - 1
+    n_tok = _i32(T, max(1, min(T, 40) - 1))
+    at = c.table[0, 2].long(), 0, 7
+    c.mass[at] = 2.0
+    ref = _mass_of(c, q, lse, n_tok)
+    c.k[at] = 0
+    c.k[at[0], 0, 7, 0] = math.inf
+    got = _mass_of(c, q, lse, n_tok)
+    assert float(got[at]) == 2.0
+    got[at] = ref[at]
+    assert torch.equal(got, ref)
+    # rows that saw nothing
+    lse[0, :, :] = -math.inf
+    q[0, :, :, 0] *= -1
+    c.k[at[0], 0, 7, 1] = math.nan
+    got = _mass_of(c, q, lse, n_tok)
+    assert torch.equal(got[c.table[0, :8].long()], c.mass[c.table[0, :8].long()])
