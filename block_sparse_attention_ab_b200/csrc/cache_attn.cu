@@ -273,10 +273,12 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_attn_kernel(const CacheAt
                     float mm = sm.m[0][n];
 #pragma unroll
                     for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, sm.m[w][n]);
+                    // the sum beside a maximum of -inf is 0, or NaN where every logit was: it is
+                    // added as it is, so that NaN reaches the row
                     float ll = 0.f;
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w)
-                        if (sm.m[w][n] != -INFINITY) ll += sm.l[w][n] * fast_exp2(sm.m[w][n] - mm);
+                        ll += sm.m[w][n] == -INFINITY ? sm.l[w][n] : sm.l[w][n] * fast_exp2(sm.m[w][n] - mm);
                     mt[nt][y] = mm;
                     lt[nt][y] = ll;
                     const float f = m[nt][y] == -INFINITY ? 0.f : fast_exp2(m[nt][y] - mm);
@@ -422,13 +424,13 @@ __global__ void __launch_bounds__(join_threads(kRowWarps)) cache_join_kernel(con
 #pragma unroll
             for (int sft = 16; sft; sft >>= 1) mn = fmaxf(mn, __shfl_xor_sync(~0u, mn, sft));
             mn = fmaxf(mn, mt);
-            if (mn == -INFINITY) continue;
             const float f0 = mt == -INFINITY ? 0.f : fast_exp2(mt - mn);
             const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - mn);
-            float lw = w == 0.f ? 0.f : ml.y * w;
+            float lw = ml.x == -INFINITY ? ml.y : ml.y * w;  // 0 or NaN beside -inf, as above
 #pragma unroll
             for (int sft = 16; sft; sft >>= 1) lw += __shfl_xor_sync(~0u, lw, sft);
-            lt = lt * f0 + lw;
+            lt = (mt == -INFINITY ? lt : lt * f0) + lw;
+            if (mn == -INFINITY) continue;
             mt = mn;
 #pragma unroll
             for (int v = 0; v < V; ++v) o[v] *= f0;
@@ -464,7 +466,10 @@ __global__ void __launch_bounds__(join_threads(kRowWarps)) cache_join_kernel(con
         for (int v = 0; v < V; ++v) o[v] = 0.f;
 #pragma unroll
         for (int w = 0; w < kRowWarps; ++w) {
-            if (sm_m[w] == -INFINITY) continue;
+            if (sm_m[w] == -INFINITY) {
+                lt += sm_l[w];
+                continue;
+            }
             const float f = fast_exp2(sm_m[w] - mt);
             lt += sm_l[w] * f;
 #pragma unroll

@@ -573,7 +573,8 @@ __global__ void __launch_bounds__(TileSmem<D, NH>::kThreads, 1)
                 const float mt = fmaxf(m, o.x);
                 f0 = m == -INFINITY ? 0.f : fast_exp2(m - mt);
                 f1 = o.x == -INFINITY ? 0.f : fast_exp2(o.x - mt);
-                l = (m == -INFINITY ? 0.f : l * f0) + (o.x == -INFINITY ? 0.f : o.y * f1);
+                // beside a maximum of -inf the sum is 0, or NaN where every logit was
+                l = (m == -INFINITY ? l : l * f0) + (o.x == -INFINITY ? o.y : o.y * f1);
                 m = mt;
             }
             const bool whole = pc.u0 == 0 && pc.u1 == pc.g.units;

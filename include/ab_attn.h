@@ -530,7 +530,8 @@ ab_status ab_cache_score(ab_cache c, ab_tokens q, int Hq, int T, const int32_t *
  * The new tokens' own keys and values are read from k, v, not from the cache: append the
  * accepted ones afterwards. Whatever lies in slots and rows that a sequence cannot see, a NaN
  * too, takes no part; a value that some row of a (sequence, key head) sees takes part in that sequence's
- * products, so a NaN or an infinity in a drafted token's value reaches its siblings.
+ * products, so a NaN or an infinity in a drafted token's value reaches its siblings. A row with
+ * a NaN logit is NaN, and so is its lse.
  * Every sum runs in an order that the lengths and counts fix: equal calls give equal bits.
  */
 ab_status ab_cache_attn_workspace_size(ab_cache c, int Hq, int T, int per_token, size_t *bytes);

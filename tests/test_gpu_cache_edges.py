@@ -235,3 +235,26 @@ def test_mass_of_infinite_keys(G, T, dtype):
     c.k[at[0], 0, 7, 1] = math.nan
     got = _mass_of(c, q, lse, n_tok)
     assert torch.equal(got[c.table[0, :8].long()], c.mass[c.table[0, :8].long()])
+
+
+@pytest.mark.parametrize("T,G", [(1, 2), (4, 4), (4, 10), (64, 3), (64, 5)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("L", [20, 3000])
+def test_attn_nan_reaches_the_rows_that_see_it(T, G, dtype, L):
+    """A NaN query gives a row of NaN with a NaN log-sum, however its keys are shared out; a NaN
+    key gives that to the rows of its sequence and head. No other row changes."""
+    c = HostCache([L, 200], 2, 64, 16, dtype, seed=18)
+    q, k, v = (t.cuda() for t in (c.randn(2, 2 * G, T, 64), c.randn(2, 2, T, 64), c.randn(2, 2, T, 64)))
+    out, lse = ab.cache_attn(c.to_gpu(), q, k, v, want_lse=True)
+    bad = q.clone()
+    bad[0, 1, T // 2] = math.nan
+    got, got_lse = ab.cache_attn(c.to_gpu(), bad, k, v, want_lse=True)
+    assert bool(got[0, 1, T // 2].isnan().all()) and bool(got_lse[0, 1, T // 2].isnan())
+    got[0, 1, T // 2], got_lse[0, 1, T // 2] = out[0, 1, T // 2], lse[0, 1, T // 2]
+    assert torch.equal(got, out) and torch.equal(got_lse, lse)
+    c.k[c.table[0, 1].long(), 0, :4] = math.nan
+    c.k[c.table[0, 0].long(), 0] = math.nan  # a whole page, in a call on few keys all that a warp has
+    got, got_lse = ab.cache_attn(c.to_gpu(), q, k, v, want_lse=True)
+    assert bool(got[0, :G].isnan().all()) and bool(got_lse[0, :G].isnan().all())
+    assert torch.equal(got[0, G:], out[0, G:]) and torch.equal(got[1], out[1])
+    assert torch.equal(got_lse[0, G:], lse[0, G:]) and torch.equal(got_lse[1], lse[1])
