@@ -259,9 +259,10 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const ScoreAr
             for (int i = lane; i < np; i += 32) m = fmaxf(m, sm_x[r * a.slice + i]);
 #pragma unroll
             for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+            // nothing but bad pages: a sum of 0; nothing but NaN: NaN
+            const float base = m == -INFINITY ? 0.f : m;
             float s = 0.f;
-            if (m != -INFINITY)
-                for (int i = lane; i < np; i += 32) s += exp2f(sm_x[r * a.slice + i] - m);
+            for (int i = lane; i < np; i += 32) s += exp2f(sm_x[r * a.slice + i] - base);
 #pragma unroll
             for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
             if (lane == 0) sm_st[r] = make_float2(m, s);
@@ -272,7 +273,7 @@ __global__ void __launch_bounds__(kScoreThreads) page_score_kernel(const ScoreAr
             for (int k = 0; k < cs; ++k) m = fmaxf(m, cl.map_shared_rank(sm_st, k)[r].x);
             for (int k = 0; k < cs; ++k) {
                 const float2 st = cl.map_shared_rank(sm_st, k)[r];
-                if (st.x != -INFINITY) s += st.y * exp2f(st.x - m);
+                s += st.x == -INFINITY ? st.y : st.y * exp2f(st.x - m);
             }
             sm_tot[r] = make_float2(m == -INFINITY ? 0.f : m, s > 0.f ? 1.f / s : (s == 0.f ? 0.f : s));
         }

@@ -258,3 +258,18 @@ def test_attn_nan_reaches_the_rows_that_see_it(T, G, dtype, L):
     assert bool(got[0, :G].isnan().all()) and bool(got_lse[0, :G].isnan().all())
     assert torch.equal(got[0, G:], out[0, G:]) and torch.equal(got[1], out[1])
     assert torch.equal(got_lse[0, G:], lse[0, G:]) and torch.equal(got_lse[1], lse[1])
+
+
+@pytest.mark.parametrize("pages", [5, 700])
+def test_score_nan_reaches_its_rows(pages):
+    """NaN in pages' sums makes every share of the rows over them NaN, also where a whole CTA of a
+    cluster has nothing else."""
+    c = HostCache([16 * pages - 3], 2, 64, 16, BF, seed=19)
+    q = c.randn(1, 4, 2, 64)
+    for parts in (1, 2, 4, 8, 16):
+        n = -(-pages // parts)
+        for at in {0, min(n, pages - 1), n * ((pages - 1) // n)}:
+            g = c.to_gpu()
+            g.ksum[c.table[0, at : min(pages, at + n)].long().cuda(), 0] = math.nan
+            got = ab.cache_score(g, q.cuda())
+            assert bool(got[0, 0, :, :pages].isnan().all()) and not bool(got[0, 1].isnan().any()), (parts, at)
