@@ -3,7 +3,8 @@
 // arguments from Python through ctypes took longer than they run (16 us for ab_cache_append
 // of 32 tokens, 31 us for ab_cache_attn of one token), so this binding is compiled: it checks
 // types, devices and shapes, allocates outputs and workspaces through torch's allocator on
-// the current stream, and calls the C ABI. It holds no state beside the handles' tensors.
+// the current stream, and calls the C ABI. It holds no state beside the handles' tensors, whose
+// addresses and shapes are read anew in every call.
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/extension.h>
@@ -64,6 +65,13 @@ struct Cache {
 
     Cache(Tensor k_, Tensor v_, Tensor table_, Tensor length_, OptTensor ksum_, OptTensor mass_, OptTensor pos_)
         : k(k_), v(v_), table(table_), length(length_), ksum(ksum_), mass(mass_), pos(pos_)
+    {
+        read();
+    }
+
+    // Check the tensors and take their addresses: at every call, because a tensor may have been set
+    // to other memory since the last one (an emptied and refilled storage, set_, .data).
+    void read()
     {
         for (const Tensor *t : {&k, &v}) {
             const char *n = t == &k ? "k" : "v";
@@ -158,9 +166,10 @@ Plan plan_of(const Cache &x, int64_t T, const OptTensor &idx, const OptTensor &c
     return p;
 }
 
-void append(const Cache &x, const Tensor &k, const Tensor &v, const OptTensor &n_new, const OptTensor &sel,
+void append(Cache &x, const Tensor &k, const Tensor &v, const OptTensor &n_new, const OptTensor &sel,
             const OptTensor &start, const OptTensor &pos, const OptTensor &dev_flag)
 {
+    x.read();
     const ab_tokens tk = x.tokens(k, x.c.Hk, "k"), tv = x.tokens(v, x.c.Hk, "v");
     if (v.size(2) != k.size(2)) bad_value("k and v must have one shape");
     const int T = (int)k.size(2);
@@ -171,9 +180,10 @@ void append(const Cache &x, const Tensor &k, const Tensor &v, const OptTensor &n
           "ab_cache_append");
 }
 
-Tensor score(const Cache &x, const Tensor &q, const OptTensor &n_tok, bool per_token, int first, int recent,
+Tensor score(Cache &x, const Tensor &q, const OptTensor &n_tok, bool per_token, int first, int recent,
              const OptTensor &out, const OptTensor &dev_flag)
 {
+    x.read();
     const ab_tokens tq = x.tokens(q, -1, "q");
     Cache::On on(x.dev);
     const int64_t T = q.size(2);
@@ -185,18 +195,20 @@ Tensor score(const Cache &x, const Tensor &q, const OptTensor &n_tok, bool per_t
     return o;
 }
 
-size_t attn_workspace(const Cache &x, int Hq, int T, bool per_token)
+size_t attn_workspace(Cache &x, int Hq, int T, bool per_token)
 {
+    x.read();
     size_t n = 0;
     check(ab_cache_attn_workspace_size(x.c, Hq, T, per_token, &n), "ab_cache_attn_workspace_size");
     return n;
 }
 
-py::object attn(const Cache &x, const Tensor &q, const OptTensor &k, const OptTensor &v, const OptTensor &n_tok,
+py::object attn(Cache &x, const Tensor &q, const OptTensor &k, const OptTensor &v, const OptTensor &n_tok,
                 const OptTensor &tree, const OptTensor &idx, const OptTensor &cnt, const OptTensor &w, bool want_lse,
                 const OptTensor &out, const std::optional<at::ScalarType> &out_type, const OptTensor &workspace,
                 const OptTensor &dev_flag)
 {
+    x.read();
     const ab_tokens tq = x.tokens(q, -1, "q");
     const int64_t B = x.c.B, Hq = q.size(1), T = q.size(2), d = x.c.d;
     if (!k != !v) bad_value("k and v go together");
@@ -227,10 +239,11 @@ py::object attn(const Cache &x, const Tensor &q, const OptTensor &k, const OptTe
     return py::cast(o);
 }
 
-Tensor mass(const Cache &x, const Tensor &q, const Tensor &lse, const OptTensor &n_tok, const OptTensor &sel,
+Tensor mass(Cache &x, const Tensor &q, const Tensor &lse, const OptTensor &n_tok, const OptTensor &sel,
             const OptTensor &idx, const OptTensor &cnt, const OptTensor &w, const OptTensor &out,
             const OptTensor &dev_flag)
 {
+    x.read();
     const ab_tokens tq = x.tokens(q, -1, "q");
     if (!x.mass) bad_value("the cache has no mass");
     const int64_t B = x.c.B, Hq = q.size(1), T = q.size(2);
@@ -245,9 +258,10 @@ Tensor mass(const Cache &x, const Tensor &q, const Tensor &lse, const OptTensor 
     return out ? *out : *x.mass;
 }
 
-py::tuple keep(const Cache &x, int64_t budget, int64_t recent, const OptTensor &next_pos, const OptTensor &score,
+py::tuple keep(Cache &x, int64_t budget, int64_t recent, const OptTensor &next_pos, const OptTensor &score,
                const OptTensor &pos, const OptTensor &length, const OptTensor &workspace, const OptTensor &dev_flag)
 {
+    x.read();
     // before they are cut to the 32 bits of the C ABI: src is allocated from the whole budget
     if (budget < 1 || budget > INT32_MAX) bad_value("budget must be 1 .. 2^31 - 1");
     if (recent < 0 || recent > INT32_MAX) bad_value("recent must be 0 .. 2^31 - 1");
@@ -268,8 +282,9 @@ py::tuple keep(const Cache &x, int64_t budget, int64_t recent, const OptTensor &
     return py::make_tuple(src, n);
 }
 
-void compact(const Cache &x, const Tensor &src, const Tensor &n_keep, const OptTensor &dev_flag)
+void compact(Cache &x, const Tensor &src, const Tensor &n_keep, const OptTensor &dev_flag)
 {
+    x.read();
     if (src.dim() != 3 || src.size(2) > INT32_MAX) bad_value("src must be [B, Hk, budget]");
     Cache::On on(x.dev);
     check(ab_cache_compact(x.c, (int)src.size(2),

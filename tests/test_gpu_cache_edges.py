@@ -273,3 +273,27 @@ def test_score_nan_reaches_its_rows(pages):
             g.ksum[c.table[0, at : min(pages, at + n)].long().cuda(), 0] = math.nan
             got = ab.cache_score(g, q.cuda())
             assert bool(got[0, 0, :, :pages].isnan().all()) and not bool(got[0, 1].isnan().any()), (parts, at)
+
+
+def test_handle_follows_its_tensors():
+    """Tensors of a handle that are set to other memory (an offloaded cache that comes back, say)."""
+    c = HostCache([100, 30], 2, 64, 32, BF, spare=4, seed=15)
+    for b in range(2):
+        c.allocate(b, 128)
+    g, other = c.to_gpu(), c.to_gpu()
+    old = {n: getattr(g, n).clone() for n in ("k", "v", "length", "ksum", "mass", "pos")}
+    kept = [getattr(g, n).detach() for n in old]  # the first memory lives on
+    for n in old:
+        getattr(g, n).set_(getattr(other, n).clone())
+    q, k, v = c.randn(2, 4, 1, 64).cuda(), c.randn(2, 2, 1, 64).cuda(), c.randn(2, 2, 1, 64).cuda()
+    ab.cache_append(g, k, v)
+    ab.cache_append(other, k, v)
+    for n, t in zip(old, kept):
+        assert torch.equal(t, old[n]), n
+        assert torch.equal(getattr(g, n), getattr(other, n)), n
+    g.length.set_(torch.zeros(3, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError, match="length must be"):
+        ab.cache_attn(g, q)
+    g.k.set_(torch.empty(0, dtype=BF, device="cuda"))  # no pages to read
+    with pytest.raises(ValueError, match="k must be"):
+        ab.cache_append(g, k, v)
