@@ -297,3 +297,43 @@ def test_handle_follows_its_tensors():
     g.k.set_(torch.empty(0, dtype=BF, device="cuda"))  # no pages to read
     with pytest.raises(ValueError, match="k must be"):
         ab.cache_append(g, k, v)
+
+
+@pytest.mark.parametrize("Hk,G,T,d,page", [(2, 4, 20, 128, 32), (1, 5, 64, 64, 16), (2, 3, 90, 128, 128),
+                                           (1, 24, 3, 64, 64)])
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("use", ["all", "plan"])
+def test_tiles_read_nothing_behind_a_sequence(Hk, G, T, d, page, dtype, use):
+    """The tensor-core kernels copy whole tiles: NaN in every row that no sequence owns and in
+    tokens behind n_tok changes nothing."""
+    c = HostCache([45, 100, 0, 7 * page + 3, 2 * page], Hk, d, page, dtype, spare=3, seed=16)
+    B = c.B
+    q, k, v = c.randn(B, Hk * G, T, d), c.randn(B, Hk, T, d), c.randn(B, Hk, T, d)
+    n = [T, max(1, T - 1), 1, T // 2, 0]
+    idx = torch.full((B, Hk, 1, c.max_pages), -1, dtype=torch.int32)
+    idx[..., :3] = torch.tensor([0, 1, 7])  # the last pages of some, behind others
+    cnt = torch.full((B, Hk, 1), 3, dtype=torch.int32)
+    plan = (idx.cuda(), cnt.cuda()) if use == "plan" else (None, None)
+
+    def run():
+        g = c.to_gpu()
+        out, lse = ab.cache_attn(g, q.cuda(), k.cuda(), v.cuda(), n_tok=_i32(*n), idx=plan[0], cnt=plan[1],
+                                 want_lse=True)
+        m = torch.full_like(g.mass, 7.0)
+        ab.cache_mass(g, q.cuda(), lse, n_tok=_i32(*[min(a, int(b)) for a, b in zip(n, c.length)]), out=m)
+        return out.cpu(), lse.cpu(), m.cpu()
+
+    ref = run()
+    owned = torch.zeros(c.n_pages, page, dtype=torch.bool)
+    for b in range(B):
+        s = torch.arange(int(c.length[b]))
+        owned[c.table[b, s // page].long(), s % page] = True
+    assert bool((~owned).any())
+    for bad in (math.nan, math.inf):
+        for t in (c.k, c.v):
+            t.permute(0, 2, 1, 3)[~owned] = bad
+        for b in range(B):
+            for t in (k, v, q):
+                t[b, :, n[b]:] = bad
+        for a, e in zip(run(), ref):
+            assert torch.equal(a, e) and not bool(a.isnan().any())
