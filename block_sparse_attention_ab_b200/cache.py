@@ -6,7 +6,8 @@ serving step over a cache, with block-sparse attention and a bounded number of s
   scores = cache_score(c, q)                       # cheap page scores for the new tokens
   idx, cnt, w = select(scores, budget, "sip")      # the pages to read
   out, lse = cache_attn(c, q, k, v, idx=idx, cnt=cnt, w=w, want_lse=True)
-  cache_append(c, k, v)                            # (sel=: the accepted tokens of a tree)
+  cache_append(c, k, v, pos=next_pos)              # (sel=: the accepted tokens of a tree)
+  next_pos += 1                                    # by the tokens appended; evictions change nothing
   cache_mass(c, q, lse, idx=idx, cnt=cnt, w=w)     # the weight every slot received
   src, n = cache_keep(c, slots, recent=64, next_pos=next_pos)
   cache_compact(c, src, n)                         # evict down to `slots`
@@ -115,14 +116,17 @@ def make_cache(B: int, Hk: int, d: int, n_pages: int, max_pages: int, page: int 
 def cache_append(cache: KVCache, k, v, n_new=None, sel=None, start=None, pos=None, dev_flag=None):
     """Write new tokens' keys and values (rows sel[b, i] of k and v [B, Hk, T, d], or rows
     0 .. n_new[b] - 1) at slot start[b] (default: the sequence's end) and set length. pos int32
-    [B]: the first new token's position (default: its slot)."""
+    [B]: the first new token's position (default: its slot, which is its position only while
+    nothing has been evicted)."""
     cache._c.append(k, v, n_new, sel, start, pos, dev_flag)
 
 
 def cache_score(cache: KVCache, q, n_tok=None, per_token: bool = True, first: int = 0, recent: int = 0,
                 out=None, dev_flag=None):
     """Page scores fp32 [B, Hk, T or 1, max_pages] of the tokens q [B, Hq, T, d], for select().
-    The first `first` and last `recent` pages score 2: they are always kept."""
+    The first `first` and last `recent` pages score 2: they are always kept. cache_compact moves
+    the newest tokens into holes anywhere, so after an eviction the last pages are not the newest
+    tokens' any more."""
     return cache._c.score(q, n_tok, per_token, first, recent, out, dev_flag)
 
 

@@ -493,7 +493,8 @@ ab_status ab_cache_append(ab_cache c, ab_tokens k, ab_tokens v, int T, const int
  *   scores[b][hk][t][p] = 1/G sum_{h in group hk} softmax_p(x_{h,t,.})  over the valid pages,
  * so a row sums to 1, as ab_score's do, and goes to ab_select as it is (nkb = max_pages).
  * The first `first` and last `recent` valid pages score 2, which SIP and top-k always keep
- * while the budget is above their number. Pages behind the sequence score 0.
+ * while the budget is above their number. Pages behind the sequence score 0. The last pages
+ * are the newest tokens' until ab_cache_compact moves some of those into holes below.
  * q        : [B, Hq, T, d] of the cache's type. Hq: a multiple of Hk. T: 1 .. AB_MAX_TREE.
  * n_tok    : int32 [B] valid tokens per sequence, or NULL for T; rows behind score 0.
  * per_token: nonzero: one row per token, scores [B, Hk, T, max_pages]; zero: one row for all

@@ -337,3 +337,18 @@ def test_tiles_read_nothing_behind_a_sequence(Hk, G, T, d, page, dtype, use):
                 t[b, :, n[b]:] = bad
         for a, e in zip(run(), ref):
             assert torch.equal(a, e) and not bool(a.isnan().any())
+
+
+def test_readme_loop_keeps_the_newest_tokens():
+    """README's generation loop, run as it stands past its first evictions."""
+    with open(os.path.join(os.path.dirname(HERE), "README.md")) as f:
+        text = f.read()
+    text = text[text.index("# generation over a key/value cache"):]
+    scope = {"torch": torch, "ab": ab}
+    exec(text[: text.index("\n\n")], scope)
+    c, next_pos = scope["c"], scope["next_pos"]
+    assert c.length.tolist() == [4096, 4096] and next_pos.tolist() == [4106, 4106]
+    for b in range(2):
+        pos = c.pos[c.table[b, :32].long()].transpose(0, 1).reshape(8, 4096).sort(-1).values
+        assert bool((pos[:, 1:] > pos[:, :-1]).all())  # no position twice
+        assert torch.equal(pos[:, -64:], torch.arange(4106 - 64, 4106, device="cuda").int().expand(8, -1))
