@@ -352,3 +352,54 @@ def test_readme_loop_keeps_the_newest_tokens():
         pos = c.pos[c.table[b, :32].long()].transpose(0, 1).reshape(8, 4096).sort(-1).values
         assert bool((pos[:, 1:] > pos[:, :-1]).all())  # no position twice
         assert torch.equal(pos[:, -64:], torch.arange(4106 - 64, 4106, device="cuda").int().expand(8, -1))
+
+
+@pytest.mark.parametrize("T", [1, 12])
+def test_generation_with_eviction_captured_and_replayed(T):
+    """Append, mass, selection of the kept slots and their moves in one graph; two graphs that
+    share a workspace, replayed in turn, give what eager calls give."""
+    B, Hk, G, d, page, slots = 2, 2, 3, 64, 32, 200
+
+    def fresh():
+        c = HostCache([196, 150], Hk, d, page, FP, spare=16, max_pages=8, seed=23)
+        for b in range(B):
+            c.allocate(b, 8 * page)
+        c.mass.zero_()
+        return c, c.to_gpu()
+    c, a = fresh()
+    e = fresh()[1]
+    toks = [[c.randn(B, h, T, d).cuda() for h in (Hk * G, Hk, Hk)] for _ in range(6)]
+    bufs = [[torch.zeros_like(t) for t in toks[0]] for _ in range(2)]
+    size = ab.cache_attn_workspace_bytes(a, Hk * G, T, False)
+    ws, kws = (torch.empty(n, dtype=torch.uint8, device="cuda") for n in (size, 4 * B * Hk * slots))
+
+    def step(cache, q, k, v, next_pos):
+        out, lse = ab.cache_attn(cache, q, k, v, want_lse=True, workspace=ws)
+        ab.cache_append(cache, k, v, pos=next_pos)
+        next_pos += T
+        ab.cache_mass(cache, q, lse)
+        src, n = ab.cache_keep(cache, slots, recent=2 * T, next_pos=next_pos, workspace=kws)
+        ab.cache_compact(cache, src, n)
+        return out, src, n
+
+    pa, pe = a.length.clone(), e.length.clone()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        step(fresh()[1], *bufs[0], pa.clone())
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for x in bufs:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=side):
+            outs.append(step(a, *x, pa))
+    torch.cuda.synchronize()
+    for i, t in enumerate(toks):
+        for dst, x in zip(bufs[i % 2], t):
+            dst.copy_(x)
+        graphs[i % 2].replay()
+        torch.cuda.synchronize()
+        for x, y in zip(outs[i % 2], step(e, *t, pe)):
+            assert torch.equal(x, y)
+        for x in ("k", "v", "ksum", "mass", "pos", "length"):
+            assert torch.equal(getattr(a, x), getattr(e, x)), x
+    assert torch.equal(pa, pe) and a.length[0] == slots

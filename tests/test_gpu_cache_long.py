@@ -138,6 +138,12 @@ def test_attn_tiles_whole_groups():
     _attn_case(c, 24, 128, [128] * c.B, "plan_per_token", pick=[0, 31, 65])
 
 
+def test_attn_more_row_tiles_than_sms():
+    """200 tiles of 384 query rows, each one CTA's."""
+    c = Long([700, 1300], 1, 64, 32, BF, seed=7)
+    _attn_case(c, 600, 128, [128, 100], "all")
+
+
 def _attn_case(c, G, T, n_tok, use, pick=None):
     q = c.randn(c.B, c.Hk * G, T, c.d, scale=1.5)
     k = c.randn(c.B, c.Hk, T, c.d, scale=0.3)
@@ -158,7 +164,8 @@ def _attn_case(c, G, T, n_tok, use, pick=None):
     # the tensor core may truncate; then the parts of at most SMS CTAs. Each rescaling of the sums
     # by a power is one more rounding and a base-2 exponential (2^-21): at most one per unit.
     units = sum(-(-n // UNIT) + -(-T // UNIT) for n in c.lengths) * c.Hk * (T if per_token else 1)
-    U = -(-units // (SMS // (4 if G * T > 384 else 1))) + 1 if not per_token else max(c.lengths) // UNIT + 2
+    ctas = max(1, SMS // -(-G * T // 128))  # of a row tile, at least
+    U = -(-units // ctas) + 1 if not per_token else max(c.lengths) // UNIT + 2
     chain_l = (12 * U + SMS) * 2.0 ** -24 + U * 2.0 ** -21
     chain_o = (128 * U + SMS) * 2.0 ** -24 + U * 2.0 ** -21
     for b in pick if pick is not None else range(c.B):
