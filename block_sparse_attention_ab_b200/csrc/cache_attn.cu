@@ -259,7 +259,8 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_attn_kernel(const CacheAt
                     for (int sft = 4; sft < 32; sft <<= 1) ls += __shfl_xor_sync(~0u, ls, sft);
                     l[nt][y] = ls;
                     if (g == 0) {
-                        sm.m[warp][nt * 8 + 2 * c + y] = m[nt][y];
+                        // a warp whose logits were all NaN has a maximum of -inf, but takes part
+                        sm.m[warp][nt * 8 + 2 * c + y] = ls != ls ? 0.f : m[nt][y];
                         sm.l[warp][nt * 8 + 2 * c + y] = ls;
                     }
                 }
@@ -273,12 +274,10 @@ __global__ void __launch_bounds__(kThreads, OCC) cache_attn_kernel(const CacheAt
                     float mm = sm.m[0][n];
 #pragma unroll
                     for (int w = 1; w < kWarps; ++w) mm = fmaxf(mm, sm.m[w][n]);
-                    // the sum beside a maximum of -inf is 0, or NaN where every logit was: it is
-                    // added as it is, so that NaN reaches the row
                     float ll = 0.f;
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w)
-                        ll += sm.m[w][n] == -INFINITY ? sm.l[w][n] : sm.l[w][n] * fast_exp2(sm.m[w][n] - mm);
+                        if (sm.m[w][n] != -INFINITY) ll += sm.l[w][n] * fast_exp2(sm.m[w][n] - mm);
                     mt[nt][y] = mm;
                     lt[nt][y] = ll;
                     const float f = m[nt][y] == -INFINITY ? 0.f : fast_exp2(m[nt][y] - mm);
@@ -426,7 +425,7 @@ __global__ void __launch_bounds__(join_threads(kRowWarps)) cache_join_kernel(con
             mn = fmaxf(mn, mt);
             const float f0 = mt == -INFINITY ? 0.f : fast_exp2(mt - mn);
             const float w = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - mn);
-            float lw = ml.x == -INFINITY ? ml.y : ml.y * w;  // 0 or NaN beside -inf, as above
+            float lw = ml.x == -INFINITY ? ml.y : ml.y * w;  // beside -inf: 0, or NaN where every logit was
 #pragma unroll
             for (int sft = 16; sft; sft >>= 1) lw += __shfl_xor_sync(~0u, lw, sft);
             lt = (mt == -INFINITY ? lt : lt * f0) + lw;
