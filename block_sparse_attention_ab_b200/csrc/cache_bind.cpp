@@ -195,12 +195,17 @@ Tensor score(Cache &x, const Tensor &q, const OptTensor &n_tok, bool per_token, 
     return o;
 }
 
-size_t attn_workspace(Cache &x, int Hq, int T, bool per_token)
+size_t workspace_size(const Cache &x, int Hq, int T, bool per_token)
 {
-    x.read();
     size_t n = 0;
     check(ab_cache_attn_workspace_size(x.c, Hq, T, per_token, &n), "ab_cache_attn_workspace_size");
     return n;
+}
+
+size_t attn_workspace(Cache &x, int Hq, int T, bool per_token)
+{
+    x.read();
+    return workspace_size(x, Hq, T, per_token);
 }
 
 py::object attn(Cache &x, const Tensor &q, const OptTensor &k, const OptTensor &v, const OptTensor &n_tok,
@@ -228,7 +233,7 @@ py::object attn(Cache &x, const Tensor &q, const OptTensor &k, const OptTensor &
     if (want_lse) lse = x.empty({B, Hq, T}, at::kFloat);
     const void *pt = array(tree, at::kBool, {B, T, T}, x.dev, "tree");
     Tensor ws = workspace ? *workspace
-                          : x.empty({(int64_t)attn_workspace(x, (int)Hq, (int)T, p.per_token)}, at::kByte);
+                          : x.empty({(int64_t)workspace_size(x, (int)Hq, (int)T, p.per_token)}, at::kByte);
     array(ws, at::kByte, ws.sizes(), x.dev, "workspace");
     check(ab_cache_attn(x.c, tq, tk, tv, (int)Hq, (int)T, x.per_seq(n_tok, "n_tok"), (const uint8_t *)pt, p.idx,
                         p.cnt, p.w, p.per_token, po, ot == at::kFloat ? AB_F32 : (ab_dtype)x.c.dtype,
