@@ -8,8 +8,10 @@
 // fragment's own order, so a step is one 16-byte shared load per lane for two products. A
 // key's sum over rows stays in one warp: no atomics, and the same bits for equal calls. The
 // CTAs take equal runs of 64-key units of the sequences' heads in order. Bound by reading K: 16
-// sequences of 1023..32760 slots, 40 / 8 heads: 102 us, 5.6 TB/s. Three CTAs per SM took 114 us,
-// five (spilling) 144. More than 8 rows without a plan go to cache_mass_tiles.cu.
+// sequences of 1023..32760 slots, 40 / 8 heads, d = 128: 105 us, 5.4 TB/s, where the keys change
+// from call to call. CTAs per SM, on unchanged keys: three 110 us, four 99, five 120 (they spill);
+// d = 64: four 77 us, five 69, six 74, seven 86. More than 8 rows without a plan go to
+// cache_mass_tiles.cu.
 #include <cstdint>
 
 #include "cache_common.cuh"
@@ -325,7 +327,7 @@ cudaError_t launch_one(const CacheMass &a, cudaStream_t st)
 template <typename E>
 cudaError_t launch_d(const CacheMass &a, cudaStream_t st)
 {
-    return a.c.d == 64 ? launch_one<E, 64, 6>(a, st) : launch_one<E, 128, 4>(a, st);
+    return a.c.d == 64 ? launch_one<E, 64, 5>(a, st) : launch_one<E, 128, 4>(a, st);
 }
 
 }  // namespace
