@@ -17,8 +17,8 @@ struct NvtxRange {
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
-// row starts must be 16-byte aligned; strides are kept small enough that a product with an
-// index stays inside 64 bits
+// row starts must be 16-byte aligned; strides are below the 2^40 bytes that a tensor map holds.
+// (Products with an index are made in 64 bits, which is enough for any tensor in memory.)
 bool stride_ok(int64_t s) { return s % 8 == 0 && s >= 0 && s < (1ll << 38); }
 
 ab_status check_cache(const ab_cache &c, bool pages = true)

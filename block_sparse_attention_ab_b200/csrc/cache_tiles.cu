@@ -7,17 +7,17 @@
 //   warps per half, a thread per row -> P (shared memory) -> O += P V (tensor memory, fp32).
 // S leaves its buffer as soon as a half's threads have loaded it, so two buffers serve three
 // halves (their accumulators fill the other 384 of 512 columns) and every half's threads find
-// their next S waiting. What each step was worth for a 64-token tree over 8 x 16001..32760
-// slots, 40 / 8 heads (320 rows; floor 125 us): P over S's buffer, held until the second
-// product, and one warp for all copies and products 490 us; P in shared memory and four
-// independent warps 387 us; partial units by the copying warps, so that the softmax waits for S
-// alone, 350 us; those by TMA 326 us (626 TFLOP/s; 350 to 370 us where the keys change from
-// call to call). Halves of a second CTA that read K and V again took 537 us. What bounds it now:
-// the chain from S to P of each half (about 2200 cycles of a unit's 3400) and shared memory
-// bandwidth, of which the products, P and the copies use about 60%. Fetching units into L2
-// ahead, spinning or one-lane waits, a later wait for the second product and cheaper
-// exponentials changed nothing; one thread instead of a converged warp issuing the products
-// took 394 us.
+// their next S waiting. A 64-token tree over 8 x 16001..32760 slots, 40 / 8 heads (320 rows; floor
+// 125 us) takes 365 us where the keys change from call to call, 562 TFLOP/s. What each step was
+// worth, on unchanged keys: P over S's buffer, held until the second product, and one warp for
+// all copies and products 490 us; P in shared memory and four independent warps 387 us; partial
+// units by the copying warps, so that the softmax waits for S alone, 350 us; those by TMA 326 us.
+// Halves of a second CTA that read K and V again took 537 us. What bounds it now: the chain from
+// S to P of each half (a unit takes about 4100 cycles under ncu, of which the tensor core is busy
+// 43%) and shared memory bandwidth, of which the products' operands use 47% and the threads 12%.
+// Fetching units into L2 ahead, spinning or one-lane waits, a later wait for the second product
+// and cheaper exponentials changed nothing; one thread instead of a converged warp issuing the
+// products took 394 us.
 // Units whose 64 keys all exist come by TMA through a map over (d, row, head, page): the page's
 // number is a coordinate, so any strides and page sizes do, and pages of 16 and 32 tokens are 4
 // and 2 boxes of one tile. The others (a sequence's last keys, the new tokens, a tile with an

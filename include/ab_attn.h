@@ -523,7 +523,9 @@ ab_status ab_cache_score(ab_cache c, ab_tokens q, int Hq, int T, const int32_t *
  *             0 .. max_pages raises AB_FLAG_BAD_INDEX (skipped, clamped), a weight that is
  *             not finite and positive AB_FLAG_BAD_WEIGHT (its page is skipped).
  * out       : [B, Hq, T, d] contiguous, in the cache's type or AB_F32 (out_dtype); rows
- *             t >= n_tok[b] and rows that see nothing are 0. Must not overlap an input.
+ *             t >= n_tok[b] and rows that see nothing are 0. Must not overlap an input. The
+ *             probabilities are rounded to the cache's type before they meet the values (half
+ *             a step each; their sum is not), whatever out_dtype is.
  * lse       : optional fp32 [B, Hq, T]: ln of the denominator (0 for t >= n_tok[b], -inf
  *             for a row that sees nothing).
  * workspace : ab_cache_attn_workspace_size() bytes, contents need not be initialised. Calls
