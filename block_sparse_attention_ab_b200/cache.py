@@ -41,7 +41,8 @@ class TokensStruct(ctypes.Structure):
 
 
 def bind(L):
-    """Argument types of the ab_cache_* calls."""
+    """Argument types of the ab_cache_* calls, for ctypes (the functions below go through the
+    compiled binding)."""
     C, T, I, P, Z = CacheStruct, TokensStruct, ctypes.c_int, _P, ctypes.c_size_t
     size_p = ctypes.POINTER(ctypes.c_size_t)
     for name, args in {

@@ -337,7 +337,8 @@ cudaError_t launch_cache_mass(const CacheMass &a, cudaStream_t st)
     const ab_cache &c = a.c;
     // Over 8 x 16380..32760 slots of 8 heads: 8 rows 71 us here and 72 us in the tile kernel, 16
     // rows 76 and 72, 32 rows 96 and 72, 64 rows 139 and 75, 128 rows 225 and 103. The tile
-    // kernel takes no plan (of a tile's pages most would be outside it).
+    // kernel takes no plan: of a shared plan's tiles most pages would be outside it, and for plans
+    // per token, whose union may be nearly every page, it has no mask of rows by page.
     if (!a.idx && a.G * a.T > 8 && stride_maps(c.k_row, c.page) && stride_maps(c.k_head, c.Hk) &&
         stride_maps(c.k_page, c.n_pages))
         return launch_cache_mass_tiles(a, st);
