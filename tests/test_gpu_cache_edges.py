@@ -12,7 +12,7 @@ import pytest
 import torch
 
 import block_sparse_attention_ab_b200 as ab
-from cache_reference import F64, HostCache, attn, keep, mass, score
+from cache_reference import F64, HostCache, attn, mass
 
 pytestmark = pytest.mark.gpu
 
@@ -400,3 +400,74 @@ def test_generation_with_eviction_captured_and_replayed(T):
         for x in ("k", "v", "ksum", "mass", "pos", "length"):
             assert torch.equal(getattr(a, x), getattr(e, x)), x
     assert torch.equal(pa, pe) and a.length[0] == slots
+
+
+def _check(got, lse, ref, dtype):
+    out, ref_lse, tol, tol_lse = (x.cuda() for x in ref)
+    err = (got.to(F64) - out).abs()
+    assert bool((err <= tol + torch.finfo(dtype).eps / 2 * (out.abs() + tol) + 1e-7).all()), float(err.max())
+    assert bool(((lse.to(F64) - ref_lse).abs() <= tol_lse + 2.0 ** -23 * ref_lse.abs()).all())
+
+
+@pytest.mark.parametrize("T,G", [(1, 2), (9, 2), (20, 4), (64, 5), (100, 2)])
+@pytest.mark.parametrize("how", ["heads", "batch", "tokens", "all"])
+def test_attn_of_expanded_tokens(T, G, how):
+    """New tokens whose keys and values are one row seen as many (strides of 0: no tensor map)."""
+    c = HostCache([70, 0, 200], 2, 64, 32, BF, seed=24)
+    q, k, v = c.randn(3, 2 * G, T, 64), c.randn(3, 2, T, 64), c.randn(3, 2, T, 64)
+    cut = {"heads": (slice(None), slice(0, 1)), "batch": (slice(0, 1),), "all": (slice(0, 1),) * 3,
+           "tokens": (slice(None), slice(None), slice(0, 1))}[how]
+    k, v = (t[cut].expand(3, 2, T, 64) for t in (k, v))
+    kg, vg = (t[cut].cuda().expand(3, 2, T, 64) for t in (k, v))
+    qg = q[:1].cuda().expand(3, -1, -1, -1)
+    n = torch.tensor([T, max(1, T - 3), T // 2])
+    got, lse = ab.cache_attn(c.to_gpu(), qg, kg, vg, n_tok=n.int().cuda(), want_lse=True)
+    _check(got, lse, attn(c, q[:1].expand(3, -1, -1, -1), k, v, n), BF)
+
+
+@pytest.mark.parametrize("T,G", [(1, 1), (20, 1), (70, 5)])
+@pytest.mark.parametrize("page,d", [(16, 128), (128, 64)])
+def test_pool_of_one_page_and_one_head(T, G, page, d):
+    """Dimensions of one element, whose strides mean nothing."""
+    c = HostCache([page - 3], 1, d, page, FP, seed=25, max_pages=1)
+    used = int(c.table[0, 0])
+    c.k, c.v, c.mass, c.n_pages = c.k[used : used + 1], c.v[used : used + 1], c.mass[used : used + 1] * 0, 1
+    c.pos, c.ksum = c.pos[:1], c.ksum[:1]
+    c.table[0, 0] = 0
+    g = c.to_gpu()
+    q, k, v = c.randn(1, G, T, d), c.randn(1, 1, T, d), c.randn(1, 1, T, d)
+    got, lse = ab.cache_attn(g, q.cuda(), k.cuda(), v.cuda(), want_lse=True)
+    _check(got, lse, attn(c, q, k, v), FP)
+    n = min(T, page - 3)
+    ab.cache_mass(g, q.cuda(), lse, n_tok=_i32(n))
+    ref, tol = mass(c, q, lse.cpu(), [n])
+    assert bool(((g.mass.cpu().to(F64) - ref).abs() <= tol + 1e-7).all())
+
+
+@pytest.mark.parametrize("T", [1, 40])
+def test_keys_and_values_side_by_side(T):
+    """Keys and values in one buffer [n_pages, page, 2, Hk, d], other pages of it in use elsewhere."""
+    c = HostCache([333, 64, 7], 3, 128, 64, BF, spare=5, seed=26)
+    for b in range(3):
+        c.allocate(b, int(c.length[b]) + T)
+    buf = torch.full((c.n_pages + 2, 64, 2, 3, 128), math.nan, dtype=BF, device="cuda")
+    k, v = (buf[1:-1, :, i].transpose(1, 2) for i in range(2))
+    k.copy_(c.k)
+    v.copy_(c.v)
+    g = ab.KVCache(k=k, v=v, table=c.table.cuda(), length=c.length.cuda(), ksum=c.ksum.cuda(),
+                   mass=torch.zeros(c.n_pages, 3, 64, device="cuda"))
+    q, kn, vn = c.randn(3, 6, T, 128), c.randn(3, 3, T, 128), c.randn(3, 3, T, 128)
+    got, lse = ab.cache_attn(g, q.cuda(), kn.cuda(), vn.cuda(), want_lse=True)
+    _check(got, lse, attn(c, q, kn, vn), BF)
+    ab.cache_append(g, kn.cuda(), vn.cuda())
+    for b in range(3):
+        s = torch.arange(int(c.length[b]), int(c.length[b]) + T)
+        at = (c.table[b, s // 64].long(), slice(None), s % 64)
+        c.k[at], c.v[at] = kn[b].transpose(0, 1), vn[b].transpose(0, 1)
+    assert torch.equal(k.cpu(), c.k) and torch.equal(v.cpu(), c.v)
+    assert bool(buf[0].isnan().all()) and bool(buf[-1].isnan().all())
+    c.length += T
+    c.mass.zero_()
+    ab.cache_mass(g, q.cuda(), lse)
+    ref, tol = mass(c, q, lse.cpu())
+    assert bool(((g.mass.cpu().to(F64) - ref).abs() <= tol + 1e-7).all())
