@@ -118,7 +118,8 @@ def cache_append(cache: KVCache, k, v, n_new=None, sel=None, start=None, pos=Non
     """Write new tokens' keys and values (rows sel[b, i] of k and v [B, Hk, T, d], or rows
     0 .. n_new[b] - 1) at slot start[b] (default: the sequence's end) and set length. pos int32
     [B]: the first new token's position (default: its slot, which is its position only while
-    nothing has been evicted)."""
+    nothing has been evicted). With start, no array may lie in cache.length, which the call
+    writes; give clones of it."""
     cache._c.append(k, v, n_new, sel, start, pos, dev_flag)
 
 
